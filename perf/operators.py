@@ -225,7 +225,7 @@ def prepare(case, seed):
         if op == "weights":
             s["ws"] = bmw.WeightsWorkspace(s["cfg"], case["rows"])
         if op == "evict":
-            s["ws"] = bmw.EvictWorkspace(s["cfg"], case["budget"])
+            s["ws"] = bmw.EvictWorkspace(s["cfg"])
     return s
 
 
