@@ -21,7 +21,12 @@ __all__ = [
     "la_pbd_selftest_timeout", "la_pbd_selftest_replan", "la_block_prefill_selftest_timeout",
     "la_pbd_step_varwin", "la_block_prefill", "la_block_prefill_workspace_bytes",
     "la_pbd_attn_paged", "la_pbd_step_paged", "Workspace", "PrefillWorkspace",
-    "EXPORTED_SYMBOLS",
+    "LA_ROPE_HALF", "LA_ROPE_INTERLEAVED", "LA_ROPE_SCALE_NONE", "LA_ROPE_SCALE_LINEAR",
+    "LA_ROPE_SCALE_BASE", "LA_ROPE_SCALE_PAIRS", "LA_ROPE_SCALE_TURNS", "RopePlan", "la_rope",
+    "la_rope_plan_init", "la_rope_append", "la_rope_append_paged", "la_pbd_attn_weights",
+    "la_pbd_attn_weights_paged", "la_pbd_attn_weights_workspace_bytes", "WeightsWorkspace",
+    "la_kv_evict", "la_kv_evict_paged", "la_kv_evict_workspace_bytes", "EvictWorkspace",
+    "la_pbd_verify", "EXPORTED_SYMBOLS",
 ]
 
 LA_MASK_PBD = 0
@@ -29,6 +34,17 @@ LA_MASK_CAUSAL_WINDOW = 1
 LA_ALGO_AUTO = 0
 LA_ALGO_TCGEN05 = 1
 LA_ALGO_SIMT = 2
+
+LA_ROPE_HALF = 0
+LA_ROPE_INTERLEAVED = 1
+LA_ROPE_SCALE_NONE = 0
+LA_ROPE_SCALE_LINEAR = 1
+LA_ROPE_SCALE_BASE = 2
+LA_ROPE_SCALE_PAIRS = 3
+LA_ROPE_SCALE_TURNS = 4
+LA_DTYPE_BF16 = 0
+LA_DTYPE_F16 = 1
+LA_DTYPE_F32 = 2
 
 LA_OK = 0
 LA_ERR_INVALID_ARG_CODE = 1
@@ -42,7 +58,11 @@ EXPORTED_SYMBOLS = ["la_version", "la_status_string", "la_pbd_workspace_bytes",
                     "la_noop_chain", "la_pbd_algo", "la_pbd_selftest_timeout",
                     "la_pbd_selftest_replan", "la_block_prefill_selftest_timeout",
                     "la_pbd_attn_varwin", "la_pbd_step_varwin", "la_block_prefill",
-                    "la_block_prefill_workspace_bytes", "la_pbd_attn_paged", "la_pbd_step_paged"]
+                    "la_block_prefill_workspace_bytes", "la_pbd_attn_paged", "la_pbd_step_paged",
+                    "la_rope_plan_init", "la_rope", "la_rope_append", "la_rope_append_paged",
+                    "la_pbd_attn_weights", "la_pbd_attn_weights_paged",
+                    "la_pbd_attn_weights_workspace_bytes", "la_kv_evict", "la_kv_evict_paged",
+                    "la_kv_evict_workspace_bytes", "la_pbd_verify"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB: Optional[ctypes.CDLL] = None
@@ -68,6 +88,28 @@ class Config(ctypes.Structure):
         if scale is None:
             scale = 1.0 / math.sqrt(head_dim)
         return cls(batch, num_q_heads, num_kv_heads, head_dim, max_seq, scale, mask_mode, algo)
+
+
+class RopePlan(ctypes.Structure):
+    """Mirror of ``la_rope_plan``: a rotation by position, made once with ``RopePlan.make``."""
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("out_scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("turns", ctypes.c_double * 128)]
+
+    LAYOUTS = {"half": LA_ROPE_HALF, "interleaved": LA_ROPE_INTERLEAVED}
+    SCALINGS = {"none": LA_ROPE_SCALE_NONE, "linear": LA_ROPE_SCALE_LINEAR,
+                "base": LA_ROPE_SCALE_BASE, "pairs": LA_ROPE_SCALE_PAIRS,
+                "turns": LA_ROPE_SCALE_TURNS}
+
+    @classmethod
+    def make(cls, rotary_dim, base=10000.0, layout="half", scaling="none", factor=1.0,
+             original_max=1, low_turns=1.0, high_turns=32.0, out_scale=1.0) -> "RopePlan":
+        """layout and scaling by name or by their ``LA_ROPE_*`` number; see la_rope_plan_init."""
+        plan = cls()
+        la_rope_plan_init(plan, rotary_dim, cls.LAYOUTS.get(layout, layout),
+                          cls.SCALINGS.get(scaling, scaling), base, factor, original_max,
+                          low_turns, high_turns, out_scale)
+        return plan
 
 
 def library_path() -> str:
@@ -133,6 +175,36 @@ def load() -> ctypes.CDLL:
     lib.la_pbd_selftest_timeout.restype = i32
     lib.la_pbd_selftest_timeout.argtypes = [cfgp, vp, vp, vp, vp, i32, vp, vp, sz, ctypes.c_int64,
                                             vp]
+    i64, f32, f64 = ctypes.c_int64, ctypes.c_float, ctypes.c_double
+    planp = ctypes.POINTER(RopePlan)
+    lib.la_rope_plan_init.restype = i32
+    lib.la_rope_plan_init.argtypes = [planp, i32, i32, i32, f64, f64, i32, f64, f64, f32]
+    lib.la_rope.restype = i32
+    lib.la_rope.argtypes = [planp, i32, vp, i64, i64, vp, i64, i32, i32, i32, vp, i64, i64, vp]
+    lib.la_rope_append.restype = i32
+    lib.la_rope_append.argtypes = [cfgp, planp, vp, i64, vp, i64, vp, i64, vp, vp, vp, i32, vp, vp,
+                                   vp, vp, vp]
+    lib.la_rope_append_paged.restype = i32
+    lib.la_rope_append_paged.argtypes = [cfgp, planp, vp, i64, vp, i64, vp, i64, vp, i32, i32, i32,
+                                         vp, vp, vp, i32, vp, vp, vp, vp, vp]
+    lib.la_pbd_attn_weights_workspace_bytes.restype = sz
+    lib.la_pbd_attn_weights_workspace_bytes.argtypes = [cfgp, i32]
+    lib.la_pbd_attn_weights.restype = i32
+    lib.la_pbd_attn_weights.argtypes = [cfgp, vp, vp, vp, vp, vp, i32, vp, vp, f32, vp, vp, sz, vp]
+    lib.la_pbd_attn_weights_paged.restype = i32
+    lib.la_pbd_attn_weights_paged.argtypes = [cfgp, vp, vp, vp, vp, i32, i32, i32, vp, vp, i32, vp,
+                                              vp, f32, vp, vp, sz, vp]
+    lib.la_kv_evict_workspace_bytes.restype = sz
+    lib.la_kv_evict_workspace_bytes.argtypes = [cfgp]
+    lib.la_kv_evict.restype = i32
+    lib.la_kv_evict.argtypes = [cfgp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz,
+                                vp]
+    lib.la_kv_evict_paged.restype = i32
+    lib.la_kv_evict_paged.argtypes = [cfgp, vp, vp, vp, i32, i32, i32, vp, vp, i32, i32, i32, vp, vp,
+                                      vp, vp, vp, vp, vp, sz, vp]
+    lib.la_pbd_verify.restype = i32
+    lib.la_pbd_verify.argtypes = [i32, vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, i32, i32, i32, vp,
+                                  vp, vp, vp, vp]
     _LIB = lib
     return lib
 
@@ -167,7 +239,7 @@ _DTYPES = {}
 def _check_tensor(t, name, dtype_name, shape=None):
     if not _DTYPES:
         import torch
-        _DTYPES.update({"bf16": torch.bfloat16, "i32": torch.int32})
+        _DTYPES.update({"bf16": torch.bfloat16, "i32": torch.int32, "f32": torch.float32})
     if t.dtype is not _DTYPES[dtype_name]:
         raise TypeError(f"{name}: expected {dtype_name}, got {t.dtype}")
     if not t.is_cuda:
@@ -491,3 +563,309 @@ def la_pbd_step_paged(cfg: Config, q, k_new, v_new, k_pool, v_pool, block_table,
                                     _ptr(k_pool), _ptr(v_pool), _ptr(block_table), pps, page_size,
                                     num_pages, _ptr(seq_lens), W, _ptr(out), workspace.data_ptr(),
                                     workspace.nbytes, _stream(stream)), "la_pbd_step_paged")
+
+
+# ---------------------------------------------------------------- rotary positions
+def la_rope_plan_init(plan: RopePlan, rotary_dim: int, layout: int, scaling: int, base: float,
+                      factor: float, original_max: int, low_turns: float, high_turns: float,
+                      out_scale: float) -> None:
+    """Fill `plan` (host only)."""
+    _check(load().la_rope_plan_init(ctypes.byref(plan), int(rotary_dim), int(layout), int(scaling),
+                                    float(base), float(factor), int(original_max), float(low_turns),
+                                    float(high_turns), float(out_scale)), "la_rope_plan_init")
+
+
+def _on_current_device(*tensors) -> None:
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"all tensors must be on the current device (cuda:{dev}), got {t.device}")
+
+
+_NUMBERS = {}
+
+
+def _dtype_number(t, name) -> int:
+    if not _NUMBERS:
+        import torch
+        _NUMBERS.update({torch.bfloat16: LA_DTYPE_BF16, torch.float16: LA_DTYPE_F16,
+                         torch.float32: LA_DTYPE_F32})
+    if t.dtype not in _NUMBERS:
+        raise TypeError(f"{name}: expected bf16, fp16 or fp32, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    return _NUMBERS[t.dtype]
+
+
+def la_rope(plan: RopePlan, x, positions, out, inverse: bool = False, stream=None) -> None:
+    """out = x turned by position: x, out [T, H, D] (bf16, fp16 or fp32, channels contiguous),
+    positions int32 [T]. `inverse` turns back: the gradient of x from the gradient of out."""
+    num = _dtype_number(x, "x")
+    if x.dim() != 3 or out.shape != x.shape or out.dtype is not x.dtype:
+        raise ValueError(f"x, out: expected [T, H, D] of one shape and type, got {tuple(x.shape)} "
+                         f"{x.dtype} and {tuple(out.shape)} {out.dtype}")
+    T, H, D = x.shape
+    if D > 1 and (x.stride(2) != 1 or out.stride(2) != 1):
+        raise ValueError("x, out: channels must be contiguous")
+    _check_tensor(positions, "positions", "i32", (T,))
+    _on_current_device(x, positions, out)
+    _check(load().la_rope(ctypes.byref(plan), num, x.data_ptr(), x.stride(0), x.stride(1),
+                          positions.data_ptr(), T, H, D, 1 if inverse else 0, out.data_ptr(),
+                          out.stride(0), out.stride(1), _stream(stream)), "la_rope")
+
+
+def _token_stride(t, name, shape) -> int:
+    """Elements between consecutive rows of a [B, T, H, D] tensor whose heads are dense and whose
+    batch is evenly strided (a part of a fused projection's output, or contiguous)."""
+    _check_dtype_cuda(t, name)
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    B, T, H, D = shape
+    st = t.stride()
+    tok = st[1] if T > 1 else st[0] if B > 1 else H * D
+    if st[3] != 1 or (H > 1 and st[2] != D) or (B > 1 and st[0] != T * tok):
+        raise ValueError(f"{name}: heads must be dense and rows evenly strided, got strides {st}")
+    return tok
+
+
+def _check_dtype_cuda(t, name):
+    import torch
+    if t.dtype is not torch.bfloat16:
+        raise TypeError(f"{name}: expected bf16, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+
+
+def _append_strides(cfg, q, k_new, v_new, seq_lens, row_lens, pos0, q_out, key_pos, slots):
+    B, Hq, Hkv, D = cfg.batch, cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim
+    if q.dim() != 4:
+        raise ValueError(f"q: expected [B, T, Hq, D], got {tuple(q.shape)}")
+    T = int(q.shape[1])
+    strides = (_token_stride(q, "q", (B, T, Hq, D)), _token_stride(k_new, "k_new", (B, T, Hkv, D)),
+               _token_stride(v_new, "v_new", (B, T, Hkv, D)))
+    _check_tensor(q_out, "q_out", "bf16", (B, T, Hq, D))
+    for name, t in (("seq_lens", seq_lens), ("row_lens", row_lens), ("pos0", pos0)):
+        if t is not None:
+            _check_tensor(t, name, "i32", (B,))
+    if key_pos is not None:
+        _check_tensor(key_pos, "key_pos", "i32", (B, Hkv, slots))
+    return T, strides
+
+
+def la_rope_append(cfg: Config, plan: RopePlan, q, k_new, v_new, seq_lens, q_out, k_cache, v_cache,
+                   row_lens=None, pos0=None, key_pos=None, stream=None) -> None:
+    """Rotate the rows of a window or a prompt and append them: q [B, T, Hq, D] into q_out, k_new
+    [B, T, Hkv, D] into cache rows P_b + i, v_new copied there, positions into key_pos. seq_lens
+    None: P_b = 0; pos0 None: positions start at P_b."""
+    T, (sq, sk, sv) = _append_strides(cfg, q, k_new, v_new, seq_lens, row_lens, pos0, q_out, key_pos,
+                                      cfg.max_seq)
+    cache = (cfg.batch, cfg.num_kv_heads, cfg.max_seq, cfg.head_dim)
+    _check_tensor(k_cache, "k_cache", "bf16", cache)
+    _check_tensor(v_cache, "v_cache", "bf16", cache)
+    _on_current_device(q, k_new, v_new, seq_lens, q_out, k_cache, v_cache, row_lens, pos0, key_pos)
+    _check(load().la_rope_append(ctypes.byref(cfg), ctypes.byref(plan), q.data_ptr(), sq,
+                                 k_new.data_ptr(), sk, v_new.data_ptr(), sv, _ptr(seq_lens),
+                                 _ptr(row_lens), _ptr(pos0), T, q_out.data_ptr(), k_cache.data_ptr(),
+                                 v_cache.data_ptr(), _ptr(key_pos), _stream(stream)),
+           "la_rope_append")
+
+
+def _pool(cfg, k_pool, v_pool, block_table):
+    """(num_pages, page_size, pages_per_seq) of checked page pools and their table."""
+    _check_tensor(k_pool, "k_pool", "bf16")
+    _check_tensor(v_pool, "v_pool", "bf16", k_pool.shape)
+    if k_pool.dim() != 4 or k_pool.shape[1] != cfg.num_kv_heads or k_pool.shape[3] != cfg.head_dim:
+        raise ValueError(f"k_pool: expected [num_pages, {cfg.num_kv_heads}, page_size, "
+                         f"{cfg.head_dim}], got {tuple(k_pool.shape)}")
+    _check_tensor(block_table, "block_table", "i32")
+    if block_table.dim() != 2 or block_table.shape[0] != cfg.batch:
+        raise ValueError(f"block_table: expected [{cfg.batch}, pages_per_seq], got "
+                         f"{tuple(block_table.shape)}")
+    return int(k_pool.shape[0]), int(k_pool.shape[2]), int(block_table.shape[1])
+
+
+def la_rope_append_paged(cfg: Config, plan: RopePlan, q, k_new, v_new, block_table, seq_lens, q_out,
+                         k_pool, v_pool, row_lens=None, pos0=None, key_pos=None, stream=None) -> None:
+    """la_rope_append into paged caches (pools and table as in la_pbd_attn_paged)."""
+    pages, size, pps = _pool(cfg, k_pool, v_pool, block_table)
+    T, (sq, sk, sv) = _append_strides(cfg, q, k_new, v_new, seq_lens, row_lens, pos0, q_out, key_pos,
+                                      pps * size)
+    _on_current_device(q, k_new, v_new, block_table, seq_lens, q_out, k_pool, v_pool, row_lens, pos0,
+                       key_pos)
+    _check(load().la_rope_append_paged(ctypes.byref(cfg), ctypes.byref(plan), q.data_ptr(), sq,
+                                       k_new.data_ptr(), sk, v_new.data_ptr(), sv,
+                                       block_table.data_ptr(), pps, size, pages, _ptr(seq_lens),
+                                       _ptr(row_lens), _ptr(pos0), T, q_out.data_ptr(),
+                                       k_pool.data_ptr(), v_pool.data_ptr(), _ptr(key_pos),
+                                       _stream(stream)), "la_rope_append_paged")
+
+
+# ---------------------------------------------------------------- key weights and eviction
+def la_pbd_attn_weights_workspace_bytes(cfg: Config, window_len: int) -> int:
+    return int(load().la_pbd_attn_weights_workspace_bytes(ctypes.byref(cfg), int(window_len)))
+
+
+def la_kv_evict_workspace_bytes(cfg: Config) -> int:
+    return int(load().la_kv_evict_workspace_bytes(ctypes.byref(cfg)))
+
+
+class WeightsWorkspace(Workspace):
+    """A device workspace sized by ``la_pbd_attn_weights_workspace_bytes``."""
+
+    def __init__(self, cfg: Config, window_len: int, device=None):
+        n = la_pbd_attn_weights_workspace_bytes(cfg, window_len)
+        if n == 0:
+            raise LaError(2, "la_pbd_attn_weights_workspace_bytes")
+        super().__init__(cfg, window_len, device=device, nbytes=n)
+
+
+class EvictWorkspace(Workspace):
+    """A device workspace sized by ``la_kv_evict_workspace_bytes``."""
+
+    def __init__(self, cfg: Config, device=None):
+        n = la_kv_evict_workspace_bytes(cfg)
+        if n == 0:
+            raise LaError(2, "la_kv_evict_workspace_bytes")
+        super().__init__(cfg, 1, device=device, nbytes=n)
+
+
+def _check_weights(cfg, W, slots, q, seq_lens, out, weights_in, weights_out, window_lens):
+    q_shape = (cfg.batch, W, cfg.num_q_heads, cfg.head_dim)
+    w_shape = (cfg.batch, cfg.num_kv_heads, slots)
+    _check_tensor(q, "q", "bf16", q_shape)
+    _check_tensor(seq_lens, "seq_lens", "i32", (cfg.batch,))
+    _check_tensor(out, "out", "bf16", q_shape)
+    _check_tensor(weights_out, "weights_out", "f32", w_shape)
+    if weights_in is not None:
+        _check_tensor(weights_in, "weights_in", "f32", w_shape)
+    if window_lens is not None:
+        _check_tensor(window_lens, "window_lens", "i32", (cfg.batch,))
+
+
+def la_pbd_attn_weights(cfg: Config, q, k_cache, v_cache, seq_lens, window_len: int, out, weights_out,
+                        workspace: Workspace, weights_in=None, decay: float = 1.0, window_lens=None,
+                        stream=None) -> None:
+    """Window attention that also adds each key's attention weight, summed over the rows that share
+    its KV head, to decay * weights_in: weights fp32 [B, Hkv, S_max]."""
+    W = int(window_len)
+    _check_weights(cfg, W, cfg.max_seq, q, seq_lens, out, weights_in, weights_out, window_lens)
+    cache = (cfg.batch, cfg.num_kv_heads, cfg.max_seq, cfg.head_dim)
+    _check_tensor(k_cache, "k_cache", "bf16", cache)
+    _check_tensor(v_cache, "v_cache", "bf16", cache)
+    _on_current_device(q, k_cache, v_cache, seq_lens, out, weights_out, weights_in, window_lens,
+                       workspace.tensor)
+    _check(load().la_pbd_attn_weights(ctypes.byref(cfg), q.data_ptr(), k_cache.data_ptr(),
+                                      v_cache.data_ptr(), seq_lens.data_ptr(), _ptr(window_lens), W,
+                                      out.data_ptr(), _ptr(weights_in), float(decay),
+                                      weights_out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                                      _stream(stream)), "la_pbd_attn_weights")
+
+
+def la_pbd_attn_weights_paged(cfg: Config, q, k_pool, v_pool, block_table, seq_lens, window_len: int,
+                              out, weights_out, workspace: Workspace, weights_in=None,
+                              decay: float = 1.0, window_lens=None, stream=None) -> None:
+    """la_pbd_attn_weights over paged caches; weights [B, Hkv, pages_per_seq * page_size]."""
+    W = int(window_len)
+    pages, size, pps = _pool(cfg, k_pool, v_pool, block_table)
+    _check_weights(cfg, W, pps * size, q, seq_lens, out, weights_in, weights_out, window_lens)
+    _on_current_device(q, k_pool, v_pool, block_table, seq_lens, out, weights_out, weights_in,
+                       window_lens, workspace.tensor)
+    _check(load().la_pbd_attn_weights_paged(ctypes.byref(cfg), q.data_ptr(), k_pool.data_ptr(),
+                                            v_pool.data_ptr(), block_table.data_ptr(), pps, size,
+                                            pages, seq_lens.data_ptr(), _ptr(window_lens), W,
+                                            out.data_ptr(), _ptr(weights_in), float(decay),
+                                            weights_out.data_ptr(), workspace.data_ptr(),
+                                            workspace.nbytes, _stream(stream)),
+           "la_pbd_attn_weights_paged")
+
+
+def _check_evict(cfg, slots, budget, weights, seq_lens, weights_out, new_lens, key_pos, next_pos,
+                 key_pos_out, kept_slots):
+    B, Hkv = cfg.batch, cfg.num_kv_heads
+    _check_tensor(weights, "weights", "f32", (B, Hkv, slots))
+    _check_tensor(weights_out, "weights_out", "f32", (B, Hkv, slots))
+    _check_tensor(seq_lens, "seq_lens", "i32", (B,))
+    _check_tensor(new_lens, "new_lens", "i32", (B,))
+    if key_pos is not None:
+        _check_tensor(key_pos, "key_pos", "i32", (B, Hkv, slots))
+    if key_pos_out is not None:
+        _check_tensor(key_pos_out, "key_pos_out", "i32", (B, Hkv, slots))
+    if next_pos is not None:
+        _check_tensor(next_pos, "next_pos", "i32", (B,))
+    if kept_slots is not None:
+        _check_tensor(kept_slots, "kept_slots", "i32", (B, Hkv, budget))
+
+
+def la_kv_evict(cfg: Config, weights, seq_lens, budget: int, k_cache, v_cache, weights_out, new_lens,
+                workspace: Workspace, key_pos=None, next_pos=None, sink: int = 0, recent: int = 0,
+                key_pos_out=None, kept_slots=None, stream=None) -> None:
+    """Bring every sequence down to min(P_b, budget) keys per KV head: protected positions (the first
+    `sink`, the last `recent`) and the highest weights stay; kept keys beyond the new length move
+    into the evicted slots. The caches are changed in place."""
+    budget = int(budget)
+    _check_evict(cfg, cfg.max_seq, budget, weights, seq_lens, weights_out, new_lens, key_pos, next_pos,
+                 key_pos_out, kept_slots)
+    cache = (cfg.batch, cfg.num_kv_heads, cfg.max_seq, cfg.head_dim)
+    _check_tensor(k_cache, "k_cache", "bf16", cache)
+    _check_tensor(v_cache, "v_cache", "bf16", cache)
+    _on_current_device(weights, seq_lens, k_cache, v_cache, weights_out, new_lens, key_pos, next_pos,
+                       key_pos_out, kept_slots, workspace.tensor)
+    _check(load().la_kv_evict(ctypes.byref(cfg), weights.data_ptr(), _ptr(key_pos), seq_lens.data_ptr(),
+                              _ptr(next_pos), budget, int(sink), int(recent), k_cache.data_ptr(),
+                              v_cache.data_ptr(), weights_out.data_ptr(), _ptr(key_pos_out),
+                              _ptr(kept_slots), new_lens.data_ptr(), workspace.data_ptr(),
+                              workspace.nbytes, _stream(stream)), "la_kv_evict")
+
+
+def la_kv_evict_paged(cfg: Config, weights, block_table, seq_lens, budget: int, k_pool, v_pool,
+                      weights_out, new_lens, workspace: Workspace, key_pos=None, next_pos=None,
+                      sink: int = 0, recent: int = 0, key_pos_out=None, kept_slots=None,
+                      stream=None) -> None:
+    """la_kv_evict over paged caches (the workspace of a cfg with max_seq = pages_per_seq *
+    page_size)."""
+    budget = int(budget)
+    pages, size, pps = _pool(cfg, k_pool, v_pool, block_table)
+    _check_evict(cfg, pps * size, budget, weights, seq_lens, weights_out, new_lens, key_pos, next_pos,
+                 key_pos_out, kept_slots)
+    _on_current_device(weights, block_table, seq_lens, k_pool, v_pool, weights_out, new_lens, key_pos,
+                       next_pos, key_pos_out, kept_slots, workspace.tensor)
+    _check(load().la_kv_evict_paged(ctypes.byref(cfg), weights.data_ptr(), _ptr(key_pos),
+                                    block_table.data_ptr(), pps, size, pages, seq_lens.data_ptr(),
+                                    _ptr(next_pos), budget, int(sink), int(recent), k_pool.data_ptr(),
+                                    v_pool.data_ptr(), weights_out.data_ptr(), _ptr(key_pos_out),
+                                    _ptr(kept_slots), new_lens.data_ptr(), workspace.data_ptr(),
+                                    workspace.nbytes, _stream(stream)), "la_kv_evict_paged")
+
+
+# ---------------------------------------------------------------- draft verification
+def la_pbd_verify(p, q, drafts, u, sample_u, tokens, accepted, draft_lens=None, seq_lens=None,
+                  seq_lens_out=None, stream=None) -> None:
+    """Accept drafted tokens against the target's probabilities and draw the next one, from given
+    uniforms: p [B, K + 1, V], q [B, K, V] or None (bf16, fp16 or fp32, entries contiguous), drafts
+    int32 [B, K], u fp32 [B, K], sample_u fp32 [B], tokens int32 [B, K + 1], accepted int32 [B]."""
+    num = _dtype_number(p, "p")
+    if p.dim() != 3 or p.shape[1] < 1 or (p.shape[2] > 1 and p.stride(2) != 1):
+        raise ValueError(f"p: expected [B, K + 1, V] with contiguous entries, got {tuple(p.shape)} "
+                         f"strides {p.stride()}")
+    B, K, V = p.shape
+    K -= 1
+    qb = qr = 0
+    if q is not None:
+        if q.dtype is not p.dtype or not q.is_cuda or q.shape != (B, K, V) or (V > 1 and q.stride(2) != 1):
+            raise ValueError(f"q: expected [{B}, {K}, {V}] of {p.dtype} with contiguous entries, got "
+                             f"{tuple(q.shape)} {q.dtype} strides {q.stride()}")
+        qb, qr = q.stride(0), q.stride(1)
+    _check_tensor(drafts, "drafts", "i32", (B, K))
+    _check_tensor(u, "u", "f32", (B, K))
+    _check_tensor(sample_u, "sample_u", "f32", (B,))
+    _check_tensor(tokens, "tokens", "i32", (B, K + 1))
+    _check_tensor(accepted, "accepted", "i32", (B,))
+    for name, t in (("draft_lens", draft_lens), ("seq_lens", seq_lens), ("seq_lens_out", seq_lens_out)):
+        if t is not None:
+            _check_tensor(t, name, "i32", (B,))
+    _on_current_device(p, q, drafts, u, sample_u, tokens, accepted, draft_lens, seq_lens, seq_lens_out)
+    _check(load().la_pbd_verify(num, p.data_ptr(), p.stride(0), p.stride(1), _ptr(q), qb, qr,
+                                drafts.data_ptr(), _ptr(draft_lens), u.data_ptr(), sample_u.data_ptr(),
+                                B, K, V, tokens.data_ptr(), accepted.data_ptr(), _ptr(seq_lens),
+                                _ptr(seq_lens_out), _stream(stream)), "la_pbd_verify")

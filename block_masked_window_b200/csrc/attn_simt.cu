@@ -286,6 +286,8 @@ __global__ void __launch_bounds__(kThreads) pbd_attn_simt_kernel(Problem p) {
         packed.x = *reinterpret_cast<uint32_t*>(&o01);
         packed.y = *reinterpret_cast<uint32_t*>(&o23);
         *reinterpret_cast<uint2*>(p.out + out_row_offset(p, sg.b, sg.h, r) + d0) = packed;
+        if (p.lse2 && lane == 0)
+          p.lse2[((size_t)sg.b * p.Hkv + sg.h) * p.rows_pad + r] = s.m[r] + log2f(s.l[r]);
       } else {
         float* slot = slot_ptr(p, sg.slot);
         if (lane == 0) {

@@ -969,6 +969,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         if (stid < NQ) {
           const float l = (wsum[stid] + wsum[NQ + stid]) + (wsum[2 * NQ + stid] + wsum[3 * NQ + stid]);
           linv[stid] = 1.f / l;
+          if (p.lse2 && stid < p.R)
+            p.lse2[((size_t)sg.b * p.Hkv + sg.h) * p.rows_pad + stid] = rowst[cur * NQ + stid] + log2f(l);
         }
         softmax_bar();
         const int rows_w = sg.w * p.G;

@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(32 * kCombineRows, kMerge <= 4 ? 12 : 1) pbd_c
     acc.w = fmaf(w, v.w, acc.w);
   }
   const float inv = 1.f / L;
+  if (p.lse2 && lane == 0) p.lse2[(size_t)s * p.rows_pad + r] = M + log2f(L);
   __nv_bfloat162 o01 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
   __nv_bfloat162 o23 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
   uint2 packed;

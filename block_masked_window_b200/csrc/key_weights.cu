@@ -1,0 +1,317 @@
+// Attention weights of the keys, summed over the rows of a window and accumulated (the second
+// half of la_pbd_attn_weights; the attention and merge kernels before it leave each row's
+// log2-sum-exp in the workspace):
+//   weights_out[b, h, j] = (j < P_b ? decay * weights_in[b, h, j] : 0)
+//                        + sum_r 2^(scale_log2 <q_r, k_j> - lse2_r)        j in [0, P_b + W_b)
+// over the R = W * G rows r that share KV head h.
+//
+// The scores are formed again rather than stored: S^T = K Q^T per 128-key tile (tcgen05,
+// M = 128 keys, N = NQ rows, K = 128 channels), the same product as in the attention kernel.
+// A key is a TMEM lane, so with the row statistics known each thread sums its own key's NQ
+// probabilities in registers: no maximum, no exchange between threads, one store per key.
+//
+// Bound: the second reading of K (256 bytes per key against 4 to read and 4 to write of the
+// weights), from L2 as far as the attention pass left it there. The exponentials (NQ per key, 16
+// per clock and SM) take a quarter of a tile's copy time at NQ = 48.
+//
+// Plan: as the attention kernel's, without a fixed segment cost: every CTA gets the same
+// number of whole key tiles, +-1, whatever the mix of lengths.
+//
+// Roles (192 threads, 1 CTA per SM): warp 0 TMA producer (Q per segment, double-buffered; K ring),
+// warp 1 TMEM owner and MMA issuer, warps 2..5 sums. Everything up to the first product only
+// reads what was complete before the attention kernel started (the merge kernel starts after
+// every attention CTA's wait), so it runs while the merge is still working; the sums wait for it.
+// Every wait is bounded, as in the attention kernel.
+#include "pbd_common.cuh"
+#include "pbd_kernels.h"
+#include "tc_util.cuh"
+#include "tma_util.h"
+
+namespace la {
+namespace {
+
+using namespace tc;
+
+constexpr int kWThreads = 192;
+constexpr int kWStages = 4;                 // K ring: 128 KB in flight per SM
+constexpr int kWSBufs = 4;                  // S^T buffers in TMEM
+constexpr int kWHalf = kTileKeys * 128;     // one 64-channel half of a K tile
+constexpr int kWTile = 2 * kWHalf;
+
+constexpr int kWBarKFull = 0;
+constexpr int kWBarKEmpty = kWBarKFull + kWStages;
+constexpr int kWBarQFull = kWBarKEmpty + kWStages;   // [2]
+constexpr int kWBarQEmpty = kWBarQFull + 2;          // [2]
+constexpr int kWBarSFull = kWBarQEmpty + 2;
+constexpr int kWBarSEmpty = kWBarSFull + kWSBufs;
+constexpr int kWBarDrain = kWBarSEmpty + kWSBufs;
+constexpr int kWNumBars = kWBarDrain + 1;
+
+struct WLayout {
+  int k, q, bar, misc, lse, lim, pre, end;
+};
+__host__ __device__ inline WLayout w_layout(int nq, int B) {
+  WLayout L;
+  L.k = 0;
+  L.q = kWStages * kWTile;
+  L.bar = L.q + 2 * nq * 256;
+  L.misc = L.bar + (kWNumBars + 1) / 2 * 16;
+  L.lse = L.misc + 16;                      // [4 warps][nq] floats (16-byte multiples)
+  L.lim = L.lse + 4 * nq * 4;               // [4][nq] ints
+  L.pre = L.lim + 4 * nq * 4;               // [B + 1] prefix sums, 32 ints
+  L.end = L.pre + (round_up(B + 1, 4) + 32) * 4;
+  return L;
+}
+
+__host__ __device__ constexpr int w_tmem_cols(int nq) {
+  return nq <= 16 ? 64 : nq <= 32 ? 128 : nq <= 64 ? 256 : 512;
+}
+
+template <int NQ, bool LIMITS, bool PAGED>
+__global__ void __launch_bounds__(kWThreads, 1)
+    key_weights_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmq,
+                       Problem p, KeyWeights kw) {
+  constexpr int kQHalf = NQ * 128;
+  constexpr int kCols = w_tmem_cols(NQ);
+  static_assert(kWSBufs * NQ <= kCols, "TMEM columns");
+  constexpr uint32_t kIdesc = idesc_f16(128, NQ, 0, 0);
+
+  extern __shared__ __align__(1024) char smem_raw[];
+  char* base = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const WLayout L = w_layout(NQ, p.B);
+  const uint32_t sb = smem_u32(base);
+  auto bar = [&](int i) { return sb + (uint32_t)L.bar + 8u * (uint32_t)i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L.misc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(base + L.misc + 8);
+  int* pre = reinterpret_cast<int*>(base + L.pre);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  Ctl ctl{abort_flag, p.hdr, p.wait_limit_ns};
+
+  pdl_trigger();
+  // Rows R..NQ-1 of Q are zero in both buffers (TMA writes only rows < R).
+  {
+    const int per_half = (NQ - p.R) * 8;
+    for (int i = tid; i < 4 * per_half; i += kWThreads) {
+      const int half = i / per_half, c = i - half * per_half;
+      reinterpret_cast<uint4*>(base + L.q + half * kQHalf + p.R * 128)[c] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_async_smem();
+  }
+  if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmk)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmq)) : "memory");
+    for (int i = 0; i < kWNumBars; ++i) {
+      const bool sums = i >= kWBarSEmpty && i < kWBarSEmpty + kWSBufs;
+      mbar_init(bar(i), sums ? 128 : 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    *abort_flag = 0;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_slot)),
+                 "r"(kCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  // seq_lens and window_lens were complete before the attention kernel's wait (see above).
+  plan_prefix<true>(p, pre, pre + round_up(p.B + 1, 4));
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const long long T = (long long)p.Hkv * pre[p.B];
+  SegmentIter it = plan_begin(p, pre, blockIdx.x, T);
+  Segment sg;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      int g = 0, n = 0;
+      bool ok = true;
+      while (ok && it.next<true>(p, pre, blockIdx.x, sg)) {
+        const int qs = n & 1;
+        if (n > 1 && !mbar_wait(bar(kWBarQEmpty + qs), ((n >> 1) - 1) & 1, ctl)) break;
+        const uint32_t dq = sb + L.q + qs * 2 * kQHalf;
+        mbar_expect_tx(bar(kWBarQFull + qs), 2u * p.R * 128u);
+        tma_load_3d(dq, &tmq, bar(kWBarQFull + qs), 0, sg.h * p.G, sg.b * p.W);
+        tma_load_3d(dq + kQHalf, &tmq, bar(kWBarQFull + qs), 64, sg.h * p.G, sg.b * p.W);
+        ++n;
+        for (int jt = sg.j0; jt < sg.j1; jt += kTileKeys, ++g) {
+          const int ks = g % kWStages;
+          if (g >= kWStages && !mbar_wait(bar(kWBarKEmpty + ks), (g / kWStages - 1) & 1, ctl)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dk = sb + L.k + ks * kWTile, fb = bar(kWBarKFull + ks);
+          mbar_expect_tx(fb, (uint32_t)kWTile);
+          if (!PAGED) {
+            const int row = (sg.b * p.Hkv + sg.h) * p.S + jt;
+            tma_load_2d(dk, &tmk, fb, 0, row);
+            tma_load_2d(dk + kWHalf, &tmk, fb, 64, row);
+          } else {
+            // 64-row boxes; a half tile past the segment reads the segment's last page again
+            // (its rows are not used), so no table entry beyond the sequence is read.
+#pragma unroll
+            for (int hr = 0; hr < 2; ++hr) {
+              int j = min(jt + 64 * hr, sg.j1 - 1);
+              const int page = __ldcg(p.block_table + (size_t)sg.b * p.pages_per_seq + j / p.page_size);
+              const int row = (page * p.Hkv + sg.h) * p.page_size + j % p.page_size;
+              tma_load_2d(dk + hr * 8192, &tmk, fb, 0, row);
+              tma_load_2d(dk + kWHalf + hr * 8192, &tmk, fb, 64, row);
+            }
+          }
+        }
+      }
+      // The copies issued last must have landed before shared memory is released.
+      for (int back = 1; back <= kWStages && g - back >= 0; ++back)
+        mbar_drain(bar(kWBarKFull + (g - back) % kWStages), ((g - back) / kWStages) & 1, 100000000LL);
+      for (int back = 1; back <= 2 && n - back >= 0; ++back)
+        mbar_drain(bar(kWBarQFull + ((n - back) & 1)), ((n - back) >> 1) & 1, 100000000LL);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      int g = 0, n = 0;
+      bool ok = true;
+      while (ok && it.next<true>(p, pre, blockIdx.x, sg)) {
+        const int qs = n & 1;
+        if (!mbar_wait(bar(kWBarQFull + qs), (n >> 1) & 1, ctl)) break;
+        const uint32_t qb = sb + L.q + qs * 2 * kQHalf;
+        for (int jt = sg.j0; jt < sg.j1; jt += kTileKeys, ++g) {
+          const int ks = g % kWStages, s = g % kWSBufs;
+          if (!mbar_wait(bar(kWBarKFull + ks), (g / kWStages) & 1, ctl) ||
+              (g >= kWSBufs && !mbar_wait(bar(kWBarSEmpty + s), (g / kWSBufs - 1) & 1, ctl))) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t kb = sb + L.k + ks * kWTile;
+#pragma unroll
+          for (int kk = 0; kk < kHeadDim / 16; ++kk) {
+            const uint32_t ka = kb + (kk >> 2) * kWHalf + (kk & 3) * 32;
+            const uint32_t qa = qb + (kk >> 2) * kQHalf + (kk & 3) * 32;
+            umma(tmem + s * NQ, sdesc(ka, 16, 1024, 2), sdesc(qa, 16, 1024, 2), kIdesc, kk > 0);
+          }
+          umma_commit(bar(kWBarSFull + s));
+          umma_commit(bar(kWBarKEmpty + ks));
+        }
+        if (ok) umma_commit(bar(kWBarQEmpty + qs));
+        ++n;
+      }
+      umma_commit(bar(kWBarDrain));
+      mbar_drain(bar(kWBarDrain), 0, 100000000LL);
+    }
+  } else {
+    // ------------------------------------------------------------------ sums
+    // Each warp keeps its own copy of a segment's row statistics: the warps share no barrier, so
+    // one that gives up keeps no other waiting.
+    const int sub = warp & 3, row = 32 * sub + lane;
+    const uint32_t lane_addr = tmem + ((uint32_t)(32 * sub) << 16);
+    float* lse = reinterpret_cast<float*>(base + L.lse) + sub * NQ;
+    int* lim = reinterpret_cast<int*>(base + L.lim) + sub * NQ;
+    const float c2 = p.scale_log2;
+    pdl_wait();   // the merge (and so the attention) kernel is complete: lse2
+    int g = 0;
+    bool ok = true;
+    while (ok && it.next<true>(p, pre, blockIdx.x, sg)) {
+      const long long head = (long long)sg.b * p.Hkv + sg.h;
+      __syncwarp();
+      for (int q = lane; q < NQ; q += 32) {
+        // A row that takes no part (operand padding, padding of a shorter window) adds 2^-inf.
+        const bool live = q < p.R && (!LIMITS || q < sg.w * p.G);
+        lse[q] = live ? __ldcg(kw.lse2 + head * p.rows_pad + q) : INFINITY;
+        if (LIMITS) lim[q] = live ? row_limit(p, sg.n, sg.w, q) : 0;
+      }
+      __syncwarp();
+      for (int jt = sg.j0; jt < sg.j1; jt += kTileKeys, ++g) {
+        const int key = jt + row, s = g % kWSBufs;
+        const bool key_ok = key < sg.j1;
+        // Window rows start afresh: their slots may hold the weight of an earlier occupant.
+        float old = 0.f;
+        if (kw.in && key < sg.n - sg.w && key_ok) old = kw.decay * kw.in[head * p.S + key];
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(kWBarSFull + s), (g / kWSBufs) & 1, ctl));
+        if (!ok) break;
+        tc_fence_after();
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        constexpr int kChunk = NQ % 48 == 0 ? 48 : NQ % 32 == 0 ? 32 : 16;   // columns held at once
+#pragma unroll
+        for (int c = 0; c < NQ; c += kChunk) {
+          float x[kChunk];
+#pragma unroll
+          for (int e = 0; e < kChunk; e += 16) tmem_ld16(lane_addr + s * NQ + c + e, x + e);
+          tc_wait_ld();
+          if (c + kChunk >= NQ) {
+            tc_fence_before();
+            mbar_arrive(bar(kWBarSEmpty + s));
+          }
+#pragma unroll
+          for (int e = 0; e < kChunk; e += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(lse + c + e);
+            const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float pr = fast_exp2(fmaf(x[e + i], c2, -l[i]));
+              if (LIMITS) pr = key < lim[c + e + i] ? pr : 0.f;
+              sum[i] += pr;
+            }
+          }
+        }
+        if (key_ok) kw.out[head * p.S + key] = old + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
+  }
+}
+
+template <int NQ, bool LIMITS, bool PAGED>
+cudaError_t launch_w(const Problem& p, const KeyWeights& kw, const CUtensorMap& k, const CUtensorMap& q,
+                     cudaStream_t s) {
+  const size_t smem = (size_t)1024 + w_layout(NQ, p.B).end;
+  cudaError_t e = cudaFuncSetAttribute(key_weights_kernel<NQ, LIMITS, PAGED>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(key_weights_kernel<NQ, LIMITS, PAGED>, dim3(p.num_ctas), dim3(kWThreads), smem, s, k, q,
+                    p, kw);
+}
+
+}  // namespace
+
+cudaError_t launch_key_weights(const Problem& p, const KeyWeights& kw, const void* tmap_k,
+                               const void* tmap_q, cudaStream_t s) {
+  const CUtensorMap& k = *static_cast<const CUtensorMap*>(tmap_k);
+  const CUtensorMap& q = *static_cast<const CUtensorMap*>(tmap_q);
+  const bool lim = row_limits(p), paged = p.block_table != nullptr;
+#define LA_W_CASE(N)                                                          \
+  case N:                                                                     \
+    if (paged) return lim ? launch_w<N, true, true>(p, kw, k, q, s)           \
+                          : launch_w<N, false, true>(p, kw, k, q, s);         \
+    return lim ? launch_w<N, true, false>(p, kw, k, q, s)                     \
+               : launch_w<N, false, false>(p, kw, k, q, s);
+#define LA_W_CASE_WIDE(N)   /* more rows than the paged attention takes */    \
+  case N:                                                                     \
+    if (paged) return cudaErrorInvalidValue;                                  \
+    return lim ? launch_w<N, true, false>(p, kw, k, q, s)                     \
+               : launch_w<N, false, false>(p, kw, k, q, s);
+  switch (round_up(p.R, 16)) {
+    LA_W_CASE(16)
+    LA_W_CASE(32)
+    LA_W_CASE(48)
+    LA_W_CASE(64)
+    LA_W_CASE(80)
+    LA_W_CASE_WIDE(96)
+    LA_W_CASE_WIDE(112)
+    LA_W_CASE_WIDE(128)
+    default: return cudaErrorInvalidValue;
+  }
+#undef LA_W_CASE
+#undef LA_W_CASE_WIDE
+}
+
+}  // namespace la

@@ -20,7 +20,9 @@ constexpr int kMaxDevices = 64;
 int g_sm_count[kMaxDevices];
 std::mutex g_mu;
 
-cudaError_t sm_count(int* out) {
+}  // namespace
+
+cudaError_t la::sm_count(int* out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -35,6 +37,11 @@ cudaError_t sm_count(int* out) {
   *out = g_sm_count[dev];
   return cudaSuccess;
 }
+
+namespace {
+
+using la::check_cfg;
+using la::sm_count;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -94,7 +101,9 @@ cudaError_t tma_maps_for(const Problem& p, long long pool_rows, la::TmaMaps* out
   return cudaSuccess;
 }
 
-la_status check_cfg(const la_pbd_cfg* cfg, int32_t W) {
+}  // namespace
+
+la_status la::check_cfg(const la_pbd_cfg* cfg, int32_t W) {
   if (!cfg) return LA_ERR_INVALID_ARG;
   if (cfg->batch < 1 || cfg->batch > la::kMaxBatch) return LA_ERR_INVALID_ARG;
   if (cfg->num_kv_heads < 1 || cfg->num_q_heads < 1) return LA_ERR_INVALID_ARG;
@@ -116,6 +125,8 @@ la_status check_cfg(const la_pbd_cfg* cfg, int32_t W) {
   if (cfg->algo == LA_ALGO_TCGEN05 && R > 80) return LA_ERR_UNSUPPORTED;
   return LA_OK;
 }
+
+namespace {
 
 // Kernel choice for a validated configuration.
 int pick_algo(const la_pbd_cfg* cfg, int R) {
@@ -245,7 +256,8 @@ la_status attn_launch(const la_pbd_cfg* cfg, const void* q, const void* k_cache,
                       const void* v_cache, const int32_t* seq_lens,
                       const int32_t* window_lens, int32_t W, void* out, void* workspace,
                       const void* k_new, const void* v_new, void* stream,
-                      const Paging& pg = Paging(), const Selftest& st = Selftest()) {
+                      const Paging& pg = Paging(), const Selftest& st = Selftest(),
+                      const la::KeyWeights* kw = nullptr) {
   Problem p;
   fill_problem(cfg, W, &p);
   p.wait_limit_ns = st.wait_limit_ns;
@@ -266,6 +278,7 @@ la_status attn_launch(const la_pbd_cfg* cfg, const void* q, const void* k_cache,
   p.hdr = reinterpret_cast<la::WsHeader*>(ws);
   p.pre_g = reinterpret_cast<int*>(ws + la::kPrefixOffset);
   p.partials = reinterpret_cast<float*>(ws + la::kSlotsOffset);
+  p.lse2 = kw ? const_cast<float*>(kw->lse2) : nullptr;
 
   int sms = 0;
   if (sm_count(&sms) != cudaSuccess) return LA_ERR_CUDA;
@@ -274,15 +287,17 @@ la_status attn_launch(const la_pbd_cfg* cfg, const void* q, const void* k_cache,
   const int algo = pick_algo(cfg, p.R);
   if (k_new && algo != LA_ALGO_TCGEN05) return LA_ERR_INVALID_ARG;
   if (pg.block_table && algo != LA_ALGO_TCGEN05) return LA_ERR_UNSUPPORTED;
+  la::TmaMaps maps;
+  if (algo == LA_ALGO_TCGEN05 || kw) {
+    const long long pool_rows =
+        pg.block_table ? (long long)pg.num_pages * p.Hkv * pg.page_size : 0;
+    if (tma_maps_for(p, pool_rows, &maps) != cudaSuccess) return LA_ERR_CUDA;
+  }
   if (algo == LA_ALGO_TCGEN05) {
     p.k_new = static_cast<const __nv_bfloat16*>(k_new);
     p.v_new = static_cast<const __nv_bfloat16*>(v_new);
     p.kc = const_cast<__nv_bfloat16*>(p.k);
     p.vc = const_cast<__nv_bfloat16*>(p.v);
-    la::TmaMaps maps;
-    const long long pool_rows =
-        pg.block_table ? (long long)pg.num_pages * p.Hkv * pg.page_size : 0;
-    if (tma_maps_for(p, pool_rows, &maps) != cudaSuccess) return LA_ERR_CUDA;
     p.unit = la::tc_tile_keys();
     p.c_min = 1;
     p.seg_units = 0;
@@ -308,6 +323,14 @@ la_status attn_launch(const la_pbd_cfg* cfg, const void* q, const void* k_cache,
   }
   if (e != cudaSuccess) return LA_ERR_CUDA;
   e = la::launch_combine(p, s);
+  if (e != cudaSuccess) return LA_ERR_CUDA;
+  if (kw) {
+    // Whole key tiles of the cache, split evenly over at most one CTA per SM.
+    p.unit = la::tc_tile_keys();
+    p.seg_units = 0;
+    p.num_ctas = grid_for(p, sms);
+    e = la::launch_key_weights(p, *kw, &maps.k, &maps.q, s);
+  }
   return e == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 
@@ -572,6 +595,68 @@ la_status la_pbd_step_paged(const la_pbd_cfg* cfg, const void* q, const void* k_
   pg.num_pages = num_pages;
   return attn_launch(cfg, q, k_pool, v_pool, seq_lens, nullptr, W, out, workspace, k_new,
                      v_new, stream, pg);
+}
+
+// Workspace of la_pbd_attn_weights: that of la_pbd_attn, then the row statistics.
+static size_t lse_offset(const la_pbd_cfg* cfg, int32_t W) {
+  const size_t need = la_pbd_workspace_bytes(cfg, W);
+  return need == 0 ? 0 : (need + 255) / 256 * 256;
+}
+
+size_t la_pbd_attn_weights_workspace_bytes(const la_pbd_cfg* cfg, int32_t W) {
+  const size_t off = lse_offset(cfg, W);
+  if (off == 0) return 0;
+  const int rows_pad = la::round_up(W * (cfg->num_q_heads / cfg->num_kv_heads), 16);
+  return off + (size_t)cfg->batch * cfg->num_kv_heads * rows_pad * sizeof(float);
+}
+
+static la_status weights_launch(const la_pbd_cfg* cfg, const void* q, const void* k_cache,
+                                const void* v_cache, const Paging& pg, const int32_t* seq_lens,
+                                const int32_t* window_lens, int32_t W, void* out,
+                                const float* weights_in, float decay, float* weights_out,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  la_status st = check_attn_args(cfg, q, k_cache, v_cache, seq_lens, W, out, workspace, workspace_bytes);
+  if (st != LA_OK) return st;
+  if (!weights_out || !aligned(weights_out, 4) || !aligned(weights_in, 4) || !aligned(window_lens, 4) ||
+      !std::isfinite(decay))
+    return LA_ERR_INVALID_ARG;
+  if (workspace_bytes < la_pbd_attn_weights_workspace_bytes(cfg, W)) return LA_ERR_WORKSPACE;
+  la::KeyWeights kw;
+  kw.lse2 = reinterpret_cast<const float*>(static_cast<char*>(workspace) + lse_offset(cfg, W));
+  kw.in = weights_in;
+  kw.out = weights_out;
+  kw.decay = decay;
+  return attn_launch(cfg, q, k_cache, v_cache, seq_lens, window_lens, W, out, workspace, nullptr, nullptr,
+                     stream, pg, Selftest(), &kw);
+}
+
+la_status la_pbd_attn_weights(const la_pbd_cfg* cfg, const void* q, const void* k_cache,
+                              const void* v_cache, const int32_t* seq_lens,
+                              const int32_t* window_lens, int32_t W, void* out,
+                              const float* weights_in, float decay, float* weights_out,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  return weights_launch(cfg, q, k_cache, v_cache, Paging(), seq_lens, window_lens, W, out, weights_in, decay,
+                        weights_out, workspace, workspace_bytes, stream);
+}
+
+la_status la_pbd_attn_weights_paged(const la_pbd_cfg* cfg, const void* q, const void* k_pool,
+                                    const void* v_pool, const int32_t* block_table,
+                                    int32_t pages_per_seq, int32_t page_size, int32_t num_pages,
+                                    const int32_t* seq_lens, const int32_t* window_lens, int32_t W,
+                                    void* out, const float* weights_in, float decay,
+                                    float* weights_out, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  la_status st = check_cfg(cfg, W);
+  if (st != LA_OK) return st;
+  st = check_paging(cfg, W, block_table, pages_per_seq, page_size, num_pages);
+  if (st != LA_OK) return st;
+  Paging pg;
+  pg.block_table = block_table;
+  pg.pages_per_seq = pages_per_seq;
+  pg.page_size = page_size;
+  pg.num_pages = num_pages;
+  return weights_launch(cfg, q, k_pool, v_pool, pg, seq_lens, window_lens, W, out, weights_in, decay,
+                        weights_out, workspace, workspace_bytes, stream);
 }
 
 la_status la_pbd_selftest_timeout(const la_pbd_cfg* cfg, const void* q, const void* k_cache,

@@ -1,0 +1,252 @@
+// Verification of a window's drafted tokens against the target's probabilities, from given
+// random numbers (la_pbd_verify). For sequence b with drafts x_0 .. x_{k-1}, target rows p_i, draft
+// rows q_i and uniforms u_i, v:
+//   draft i is accepted while u_i q_i(x_i) < p_i(x_i); n = number accepted before the first miss;
+//   the next token is drawn from r = max(p_n - q_n, 0) (from p_n when n = k, or when r sums to 0):
+//   the smallest j with r_0 + ... + r_j > v (r_0 + r_1 + ...).
+// A token drawn this way has the target's distribution whatever the drafts' is. Without q the
+// drafts are certain: accepted while u_i < p_i(x_i), and r is p_n without x_n.
+//
+// Everything is computed in 64 bits: the accept test is then exact (a product of two 24-bit
+// numbers), and a border of the cumulative sum moves by 1e-16 of the total, not by the 1e-7 at which
+// the neighbour's token comes out once in a thousand draws over 150,000 entries.
+//
+// Bound: memory, one row of p and one of q per sequence, read once. A cluster of C CTAs shares a
+// sequence: each warp sums one contiguous range of the row (loads coalesced, 8 + 8 in flight
+// a lane), the ranges' sums meet through distributed shared memory, and the CTA that owns the range
+// in which the draw falls goes over that range alone again (1/(32 C) of the row, from L2).
+#include <cooperative_groups.h>
+
+#include "pbd_common.cuh"
+#include "pbd_kernels.h"
+
+namespace la {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kVThreads = 1024;
+constexpr int kVWarps = kVThreads / 32;
+constexpr int kVMaxCtas = 8;
+constexpr int kVUnroll = 8;
+
+__device__ __forceinline__ double to_f64(float x) { return (double)x; }
+__device__ __forceinline__ double to_f64(__nv_bfloat16 x) { return (double)__bfloat162float(x); }
+__device__ __forceinline__ double to_f64(__half x) { return (double)__half2float(x); }
+__device__ __forceinline__ double positive(double x) { return x > 0.0 ? x : 0.0; }   // (NaN: 0)
+
+template <typename E>
+__global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyProblem a) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  __shared__ double s_sum[2][kVWarps];     // ranges of this CTA (a buffer per attempt)
+  __shared__ double s_scan[kVWarps];
+  __shared__ double s_total, s_before;
+  __shared__ int s_n, s_len, s_range, s_first, s_last;
+  const int b = blockIdx.x / C;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_trigger();
+  pdl_wait();
+  const E* p = static_cast<const E*>(a.p) + (long long)b * a.p_batch;
+  const E* q = a.q ? static_cast<const E*>(a.q) + (long long)b * a.q_batch : nullptr;
+  const int* drafts = a.drafts + (long long)b * a.K;
+  if (warp == 0) {
+    const int len = a.draft_lens ? __ldg(a.draft_lens + b) : a.K;
+    bool ok = false;
+    if (lane < a.K && lane < len) {
+      const int x = __ldg(drafts + lane);
+      if (x >= 0 && x < a.V) {             // a token outside the vocabulary has probability 0
+        const double px = to_f64(p[(long long)lane * a.p_row + x]);
+        const double qx = q ? to_f64(q[(long long)lane * a.q_row + x]) : 1.0;
+        ok = (double)__ldg(a.u + (long long)b * a.K + lane) * qx < px;
+      }
+    }
+    const uint32_t miss = ~__ballot_sync(0xffffffffu, ok);
+    if (lane == 0) {
+      s_len = len;
+      s_n = miss ? __ffs(miss) - 1 : 32;
+      s_first = 0x7fffffff;
+      s_last = -1;
+    }
+  }
+  __syncthreads();
+  const int n = s_n, len = s_len;
+  const bool valid = len >= 0 && len <= a.K;
+  int* tokens = a.tokens + (long long)b * (a.K + 1);
+  if (rank == 0) {
+    for (int i = tid; i <= a.K; i += kVThreads)
+      if (!valid || i != n) tokens[i] = valid && i < n ? __ldg(drafts + i) : -1;
+    if (tid == 0) {
+      a.accepted[b] = valid ? n : -1;
+      if (a.seq_lens_out) a.seq_lens_out[b] = a.seq_lens[b] + (valid ? n + 1 : 0);
+    }
+  }
+  if (!valid) return;                      // (the whole cluster)
+
+  const E* pr = p + (long long)n * a.p_row;
+  const bool rejected = n < len;
+  const E* qr = rejected && q ? q + (long long)n * a.q_row : nullptr;
+  const int skip = rejected && !q ? __ldg(drafts + n) : -1;
+  const int per = ((a.V + C * kVWarps - 1) / (C * kVWarps) + 31) & ~31;   // entries of a range
+  const double v = (double)__ldg(a.sample_u + b);
+  // First the residual, where a draft was rejected; then, if that is empty, p itself.
+  bool rest = rejected;
+  auto entry = [&](long long j, E x, E less) {
+    const double d = to_f64(x);
+    return positive(!rest ? d : qr ? d - to_f64(less) : j == skip ? 0.0 : d);
+  };
+  for (int attempt = 0;; ++attempt) {
+    const long long w0 = min((long long)(rank * kVWarps + warp) * per, (long long)a.V);
+    const long long w1 = min(w0 + per, (long long)a.V);
+    double sum = 0.0;
+    for (long long j0 = w0 + lane; j0 < w1; j0 += 32 * kVUnroll) {
+      E x[kVUnroll], y[kVUnroll];
+#pragma unroll
+      for (int i = 0; i < kVUnroll; ++i)
+        if (j0 + 32 * i < w1) x[i] = pr[j0 + 32 * i];
+      if (rest && qr) {
+#pragma unroll
+        for (int i = 0; i < kVUnroll; ++i)
+          if (j0 + 32 * i < w1) y[i] = qr[j0 + 32 * i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < kVUnroll; ++i) y[i] = x[i];   // (not used)
+      }
+#pragma unroll
+      for (int i = 0; i < kVUnroll; ++i)
+        if (j0 + 32 * i < w1) sum += entry(j0 + 32 * i, x[i], y[i]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) s_sum[attempt][warp] = sum;
+    cluster.sync();
+    // Every CTA finds the draw's range among the C * 32 ranges (lane l of warp 0: C of them).
+    if (warp == 0) {
+      double part[kVMaxCtas], mine = 0.0;
+#pragma unroll
+      for (int i = 0; i < kVMaxCtas; ++i) {
+        const int r = lane * C + i;
+        part[i] = i < C ? *cluster.map_shared_rank(&s_sum[attempt][r % kVWarps], r / kVWarps) : 0.0;
+      }
+#pragma unroll
+      for (int i = 0; i < kVMaxCtas; ++i) mine += part[i];
+      double incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const double total = __shfl_sync(0xffffffffu, incl, 31);
+      const double goal = v * total;
+      double run = incl - mine, before = 0.0, before_last = 0.0;
+      int range = -1, range_last = -1;     // first range that passes the goal; last with any weight
+#pragma unroll
+      for (int i = 0; i < kVMaxCtas; ++i) {
+        if (i < C && part[i] > 0.0) {
+          range_last = lane * C + i;
+          before_last = run;
+          if (range < 0 && run + part[i] > goal) {
+            range = lane * C + i;
+            before = run;
+          }
+          run += part[i];
+        }
+      }
+      const uint32_t hit = __ballot_sync(0xffffffffu, range >= 0);
+      const uint32_t any = __ballot_sync(0xffffffffu, range_last >= 0);
+      if (lane == 0) {
+        s_total = total;
+        if (!any) s_range = -1;
+      }
+      if (hit ? lane == __ffs(hit) - 1 : any && lane == 31 - __clz(any)) {
+        s_range = hit ? range : range_last;
+        s_before = hit ? before : before_last;
+      }
+    }
+    __syncthreads();
+    if (s_total > 0.0 || !rest) break;     // (the same in every CTA of the cluster)
+    rest = false;
+  }
+  const int range = s_range;
+  if (!(s_total > 0.0 && s_total < (double)INFINITY)) {
+    if (rank == 0 && tid == 0) tokens[n] = -1;   // nothing can be drawn
+  } else if (range / kVWarps == rank) {
+    // The smallest entry of the range at which the cumulative sum passes the goal (its last
+    // entry with any weight, where rounding lets none pass).
+    const double goal = v * s_total;
+    const long long w0 = (long long)range * per, w1 = min(w0 + per, (long long)a.V);
+    const int m = per > kVThreads ? 4 : 1;       // consecutive entries of a thread
+    double run = s_before;
+    for (long long c0 = w0; c0 < w1; c0 += (long long)kVThreads * m) {
+      double e[4], mine = 0.0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const long long j = c0 + (long long)tid * m + i;
+        e[i] = 0.0;
+        if (i < m && j < w1) e[i] = entry(j, pr[j], rest && qr ? qr[j] : pr[j]);
+        mine += e[i];
+      }
+      double incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == 31) s_scan[warp] = incl;
+      __syncthreads();
+      double at = run + (incl - mine);
+      for (int w = 0; w < kVWarps; ++w) {
+        if (w < warp) at += s_scan[w];
+        run += s_scan[w];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const long long j = c0 + (long long)tid * m + i;
+        if (e[i] > 0.0) {
+          atomicMax(&s_last, (int)j);
+          if (at + e[i] > goal) atomicMin(&s_first, (int)j);
+          at += e[i];
+        }
+      }
+      __syncthreads();
+      if (s_first != 0x7fffffff) break;
+    }
+    if (tid == 0) tokens[n] = s_first != 0x7fffffff ? s_first : s_last;
+  }
+  cluster.sync();   // no CTA leaves while another may read its sums
+}
+
+template <typename E>
+cudaError_t launch_verify_t(const VerifyProblem& a, int sms, cudaStream_t s) {
+  // CTAs per sequence: as many as keep two of them on every SM (the row is then read by the whole
+  // GPU however few sequences there are), but at least 4096 entries each.
+  int c = kVMaxCtas;
+  while (c > 1 && ((long long)a.B * c > 2LL * sms || (long long)(c - 1) * 4096 >= a.V)) c /= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.B * c));
+  cfg.blockDim = dim3(kVThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)c;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, verify_kernel<E>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_verify(const VerifyProblem& a, int dtype, int sms, cudaStream_t s) {
+  switch (dtype) {
+    case LA_DTYPE_F32: return launch_verify_t<float>(a, sms, s);
+    case LA_DTYPE_BF16: return launch_verify_t<__nv_bfloat16>(a, sms, s);
+    case LA_DTYPE_F16: return launch_verify_t<__half>(a, sms, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace la

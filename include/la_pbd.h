@@ -89,6 +89,33 @@ typedef struct la_pbd_cfg {
   int32_t algo;          /* LA_ALGO_*                                                       */
 } la_pbd_cfg;
 
+/* Layout of the rotated pairs of a head (la_rope_plan_init). */
+enum {
+  LA_ROPE_HALF = 0,          /* pair i is channels (i, i + rotary_dim / 2)                  */
+  LA_ROPE_INTERLEAVED = 1    /* pair i is channels (2 i, 2 i + 1)                           */
+};
+
+/* Scaling of the frequencies for contexts longer than the trained one (la_rope_plan_init). */
+enum {
+  LA_ROPE_SCALE_NONE = 0,
+  LA_ROPE_SCALE_LINEAR = 1,  /* every frequency divided by `factor`                         */
+  LA_ROPE_SCALE_BASE = 2,    /* base * factor^(rotary_dim / (rotary_dim - 2))               */
+  LA_ROPE_SCALE_PAIRS = 3,   /* divided by `factor`, ramped in over the pair index          */
+  LA_ROPE_SCALE_TURNS = 4    /* divided by `factor`, ramped in over the pair's turns        */
+};
+
+/* Element types of the operators that take more than bf16. */
+enum { LA_DTYPE_BF16 = 0, LA_DTYPE_F16 = 1, LA_DTYPE_F32 = 2 };
+
+/* A rotation, made by la_rope_plan_init and kept by the caller (plain host data, no handle). */
+typedef struct la_rope_plan {
+  int32_t rotary_dim;        /* channels of a head that turn: even, 2 .. 256                */
+  int32_t layout;            /* LA_ROPE_*                                                   */
+  float out_scale;           /* factor of the rotated channels                              */
+  int32_t reserved;
+  double turns[128];         /* turns per position of pair i < rotary_dim / 2               */
+} la_rope_plan;
+
 /* Library version as 10000*major + 100*minor + patch. */
 int32_t la_version(void);
 
@@ -357,6 +384,185 @@ la_status la_pbd_selftest_replan(const la_pbd_cfg* cfg, const void* q, const voi
                                  const void* v_new, void* k_cache, void* v_cache,
                                  const int32_t* seq_lens, int32_t window_len, void* out,
                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rotary positions.
+ *
+ * la_rope_plan_init fills `plan` (host only, no GPU work). Pair i < rotary_dim / 2 of a head at
+ * position t turns by the angle t * w_i, w_i = base^(-2 i / rotary_dim), scaled by `scaling`:
+ *   LINEAR  w_i / factor
+ *   BASE    base replaced by base * factor^(rotary_dim / (rotary_dim - 2))
+ *   PAIRS   (1 - r) w_i + r w_i / factor, r rising linearly in i from 0 at the pair that turns
+ *           high_turns times over original_max positions (rounded down, at least 0) to 1 at the
+ *           one that turns low_turns times (rounded up, at most rotary_dim - 1)
+ *   TURNS   (1 - k) w_i / factor + k w_i, k rising linearly with the pair's turns over original_max
+ *           positions, from 0 at low_turns to 1 at high_turns
+ * factor, original_max, low_turns and high_turns are read only where the scaling names them.
+ * out_scale multiplies the rotated channels (usually 1).
+ * LA_ERR_INVALID_ARG for a null plan, an odd rotary_dim or one outside [2, 256], base <= 1, factor <=
+ * 0, original_max < 1, turns that are not 0 < low < high, values that are not finite.
+ */
+la_status la_rope_plan_init(la_rope_plan* plan, int32_t rotary_dim, int32_t layout, int32_t scaling,
+                            double base, double factor, int32_t original_max, double low_turns,
+                            double high_turns, float out_scale);
+
+/*
+ * out[t, h, :] = x[t, h, :] turned by position positions[t]: with a the pair's angle and s =
+ * out_scale, y1 = s (x1 cos a - x2 sin a), y2 = s (x2 cos a + x1 sin a); channels from rotary_dim
+ * on are copied. inverse != 0 turns by -a: applied to a gradient of `out` it gives the gradient of
+ * x. Angles are formed and reduced in 64 bits for any int32 position (negative ones too), the
+ * rotation is computed in fp32 and rounded once.
+ *   x, out     [tokens, heads, head_dim] of `dtype` (LA_DTYPE_*), channels contiguous, tokens and
+ *              heads at the given strides in elements; rows of `out` must not overlap one another.
+ *              out may be x itself with the same strides, and may not overlap it otherwise
+ *   positions  device int32 [tokens]
+ *   head_dim   even, rotary_dim <= head_dim <= 256
+ * tokens = 0 is no work. Rows on 16-byte boundaries with head_dim % 16 == 0 (and rotary_dim %
+ * 16 == 0 in the half layout) are moved in 16-byte chunks; others work, more slowly.
+ */
+la_status la_rope(const la_rope_plan* plan, int32_t dtype, const void* x, int64_t x_token_stride,
+                  int64_t x_head_stride, const int32_t* positions, int64_t tokens, int32_t heads,
+                  int32_t head_dim, int32_t inverse, void* out, int64_t out_token_stride,
+                  int64_t out_head_stride, void* stream);
+
+/*
+ * Rotation and append in one launch, for a decode window or a whole prompt of `rows` rows a
+ * sequence. Row i < n_b of sequence b is at position t = pos0_b + i and goes to key slot P_b + i:
+ *   q_out[b, i, h, :]          = q[b, i, h, :] turned by t
+ *   k_cache[b, h, P_b + i, :]  = k_new[b, i, h, :] turned by t
+ *   v_cache[b, h, P_b + i, :]  = v_new[b, i, h, :]
+ *   key_pos[b, h, P_b + i]     = t                                  (key_pos may be NULL)
+ * ready for la_pbd_attn or la_block_prefill on the same stream.
+ *   q, k_new, v_new  bf16 [B, rows, heads, D], heads dense, consecutive rows (b * rows + i) at the
+ *                    given strides in elements (multiples of 8), so that they can be parts of one
+ *                    projection's output
+ *   q_out            bf16 [B, rows, Hq, D], dense; may be q itself if that is dense
+ *   seq_lens         device int32 [B] = P_b, or NULL: 0
+ *   row_lens         device int32 [B] = n_b, 0 <= n_b <= rows, or NULL: rows
+ *   pos0             device int32 [B], or NULL: P_b (positions run ahead of slots after evictions)
+ *   key_pos          device int32 [B, Hkv, S_max]
+ * Rows i >= n_b are padding: not read into any result, their rows of q_out left as they are. A
+ * sequence with P_b < 0, n_b outside [0, rows] or P_b + n_b > max_seq is left out (la_pbd_attn
+ * then flags it). The paged form writes into the pages (see la_pbd_attn_paged; S_max is
+ * pages_per_seq * page_size, any number of rows and heads); a key whose table entry names no page
+ * of the pool is not written. The plan's rotary_dim is at most D. q, k_new and v_new must not alias
+ * the caches.
+ */
+la_status la_rope_append(const la_pbd_cfg* cfg, const la_rope_plan* plan, const void* q,
+                         int64_t q_token_stride, const void* k_new, int64_t k_token_stride,
+                         const void* v_new, int64_t v_token_stride, const int32_t* seq_lens,
+                         const int32_t* row_lens, const int32_t* pos0, int32_t rows, void* q_out,
+                         void* k_cache, void* v_cache, int32_t* key_pos, void* stream);
+la_status la_rope_append_paged(const la_pbd_cfg* cfg, const la_rope_plan* plan, const void* q,
+                               int64_t q_token_stride, const void* k_new, int64_t k_token_stride,
+                               const void* v_new, int64_t v_token_stride, const int32_t* block_table,
+                               int32_t pages_per_seq, int32_t page_size, int32_t num_pages,
+                               const int32_t* seq_lens, const int32_t* row_lens, const int32_t* pos0,
+                               int32_t rows, void* q_out, void* k_pool, void* v_pool, int32_t* key_pos,
+                               void* stream);
+
+/*
+ * Bytes of workspace of la_pbd_attn_weights: that of la_pbd_attn, then one float per row (the
+ * rows' log-sum-exp). 0 where la_pbd_workspace_bytes gives 0.
+ */
+size_t la_pbd_attn_weights_workspace_bytes(const la_pbd_cfg* cfg, int32_t window_len);
+
+/*
+ * Window attention that also accumulates the weight each key received: `out` as la_pbd_attn (or,
+ * with window_lens, la_pbd_attn_varwin) gives it, the same bits, and for n = P_b + W_b
+ *   weights_out[b, h, j] = old + sum of p[r, j] over the rows r (window rows i < W_b times the
+ *                          query heads that share KV head h),     j in [0, n)
+ * with p the attention's probabilities, and old = decay * weights_in[b, h, j] for j < P_b, 0 for the
+ * window's own slots (they may hold the weight of an earlier occupant) and where weights_in is NULL.
+ * fp32 sums; entries from n on are left as they are.
+ *   weights_in, weights_out  device fp32 [B, Hkv, S_max]; the two may be the same buffer
+ *   window_lens              device int32 [B], or NULL: all window_len
+ *   workspace                la_pbd_attn_weights_workspace_bytes, header zeroed once
+ * A sequence that la_pbd_attn flags keeps its weights. The paged form is for la_pbd_attn_paged's
+ * configurations, with window_lens as well; S_max of the weights is pages_per_seq * page_size.
+ */
+la_status la_pbd_attn_weights(const la_pbd_cfg* cfg, const void* q, const void* k_cache,
+                              const void* v_cache, const int32_t* seq_lens,
+                              const int32_t* window_lens, int32_t window_len, void* out,
+                              const float* weights_in, float decay, float* weights_out,
+                              void* workspace, size_t workspace_bytes, void* stream);
+la_status la_pbd_attn_weights_paged(const la_pbd_cfg* cfg, const void* q, const void* k_pool,
+                                    const void* v_pool, const int32_t* block_table,
+                                    int32_t pages_per_seq, int32_t page_size, int32_t num_pages,
+                                    const int32_t* seq_lens, const int32_t* window_lens,
+                                    int32_t window_len, void* out, const float* weights_in,
+                                    float decay, float* weights_out, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of workspace of la_kv_evict (for the paged form, of a configuration whose max_seq is
+ * pages_per_seq * page_size). Host only; 0 for an invalid configuration.
+ */
+size_t la_kv_evict_workspace_bytes(const la_pbd_cfg* cfg);
+
+/*
+ * Eviction: brings every sequence down to L_b = min(P_b, budget) keys, chosen per KV head.
+ * Key j of [0, P_b) is protected if its position t_j < sink or t_j >= next_pos_b - recent. The L_b
+ * keys that stay are the first in the order: protected keys, then higher weights[b, h, j] (NaN counts
+ * as -infinity), equal ones by the lower slot. Kept keys in slots below L_b stay where they are;
+ * the k-th kept key at or above L_b moves into the k-th evicted slot below it (K and V rows, weight,
+ * position), so only keys that change place are touched, and the order of the slots is not kept (the
+ * attention does not depend on it). Slots from L_b on are left as they are.
+ *   weights, weights_out   device fp32 [B, Hkv, S_max]; may be the same buffer
+ *   key_pos, key_pos_out   device int32 [B, Hkv, S_max]: t_j; may be the same buffer. key_pos NULL:
+ *                          t_j = j (before a first eviction); key_pos_out NULL only if key_pos is
+ *   next_pos               device int32 [B], or NULL: P_b
+ *   kept_slots             device int32 [B, Hkv, budget] or NULL: the slot that each slot's key
+ *                          came from, -1 from L_b on
+ *   seq_lens, new_lens     device int32 [B]: P_b and L_b; may be the same buffer
+ *   budget                 1 .. S_max, sink + recent <= budget
+ *   workspace              la_kv_evict_workspace_bytes, 256-byte aligned, header zeroed once by
+ *                          la_pbd_workspace_init
+ * Buffers that are not said to be allowed the same may not overlap. With separate outputs the call
+ * can be repeated with the same result. A sequence with P_b < 0 or P_b > S_max keeps its cache and
+ * length and raises the sticky flag (la_pbd_check). The paged form moves rows between the
+ * sequence's own pages, which no other sequence may share; a row whose table entry names no page of
+ * the pool is not moved.
+ */
+la_status la_kv_evict(const la_pbd_cfg* cfg, const float* weights, const int32_t* key_pos,
+                      const int32_t* seq_lens, const int32_t* next_pos, int32_t budget, int32_t sink,
+                      int32_t recent, void* k_cache, void* v_cache, float* weights_out,
+                      int32_t* key_pos_out, int32_t* kept_slots, int32_t* new_lens, void* workspace,
+                      size_t workspace_bytes, void* stream);
+la_status la_kv_evict_paged(const la_pbd_cfg* cfg, const float* weights, const int32_t* key_pos,
+                            const int32_t* block_table, int32_t pages_per_seq, int32_t page_size,
+                            int32_t num_pages, const int32_t* seq_lens, const int32_t* next_pos,
+                            int32_t budget, int32_t sink, int32_t recent, void* k_pool, void* v_pool,
+                            float* weights_out, int32_t* key_pos_out, int32_t* kept_slots,
+                            int32_t* new_lens, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Verification of a window's drafted tokens against the target's probabilities, from given random
+ * numbers. For sequence b with k_b drafts x_i: draft i is accepted while u[b, i] * q_i(x_i) < p_i(x_i);
+ * n_b is the number accepted before the first miss. The next token is drawn from max(p_n - q_n, 0)
+ * after a miss (from p_n if that is zero everywhere), from p_n when all were accepted: the smallest
+ * j whose cumulative sum exceeds sample_u[b] times the total (the last entry with any weight if
+ * none does). Sums and comparisons in 64 bits; entries that are negative or NaN count as 0.
+ *   p            [B, num_drafts + 1, vocab] of `dtype`, entries contiguous, strides in elements
+ *   q            [B, num_drafts, vocab] likewise, or NULL: the drafts are certain (q_i(x_i) = 1)
+ *   drafts       device int32 [B, num_drafts]; one outside [0, vocab) is a miss
+ *   draft_lens   device int32 [B] = k_b, or NULL: num_drafts
+ *   u, sample_u  device fp32 [B, num_drafts] and [B], in [0, 1)
+ *   tokens       device int32 [B, num_drafts + 1]: the accepted drafts, the drawn token, then -1
+ *   accepted     device int32 [B] = n_b
+ *   seq_lens, seq_lens_out  device int32 [B], both or neither NULL, may be the same buffer:
+ *                seq_lens_out = seq_lens + n_b + 1 (the window's first row, the last accepted token,
+ *                and the n_b accepted drafts are now committed)
+ * num_drafts 0 .. 32 (0: a draw from p alone), vocab <= 2^24. k_b outside [0, num_drafts] gives
+ * accepted = -1, tokens -1 and the length unchanged; a row whose sum is zero or not finite
+ * gives -1 for the drawn token.
+ */
+la_status la_pbd_verify(int32_t dtype, const void* p, int64_t p_batch_stride, int64_t p_row_stride,
+                        const void* q, int64_t q_batch_stride, int64_t q_row_stride,
+                        const int32_t* drafts, const int32_t* draft_lens, const float* u,
+                        const float* sample_u, int32_t batch, int32_t num_drafts, int32_t vocab,
+                        int32_t* tokens, int32_t* accepted, const int32_t* seq_lens,
+                        int32_t* seq_lens_out, void* stream);
 
 /*
  * Synchronise `stream`, read and clear the workspace's sticky device-side error flags.

@@ -22,3 +22,10 @@ from .pbd import (  # noqa: F401
     window_attention_varwin,
     pbd_step_varwin,
 )
+from .cache_ops import (  # noqa: F401
+    rope_angles,
+    rotate,
+    key_weights,
+    evict,
+    verify,
+)
