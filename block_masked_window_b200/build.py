@@ -31,7 +31,7 @@ def nvcc() -> str:
 
 def command(out: str = LIB, extra=None):
     cmd = [nvcc(), "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3",
-           "-std=c++17", "-Xcompiler", "-fPIC", "-shared", "-Xptxas", "-v",
+           "-std=c++17", "--threads", "0", "-Xcompiler", "-fPIC", "-shared", "-Xptxas", "-v",
            "-I", os.path.join(ROOT, "include"), "-o", out]
     cmd += list(extra or [])
     cmd += [os.path.join(CSRC, s) for s in SOURCES]

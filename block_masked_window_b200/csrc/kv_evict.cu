@@ -27,9 +27,10 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kBins = 2048;                // of the widest pass
-constexpr int kSelTile = 4 * kSelThreads;  // keys of a pass in slot order
+constexpr int kSelKeys = 8;                // keys of a thread in a tile
+constexpr int kSelTile = kSelKeys * kSelThreads;
 
 // Unsigned key of the same order as the weight; NaN as -inf, -0 as +0.
 __device__ __forceinline__ uint32_t rank_of(float w) {
@@ -40,6 +41,7 @@ __device__ __forceinline__ uint32_t rank_of(float w) {
 
 // Inclusive prefix sum over the block (kSelThreads threads). Two barriers.
 __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_tot, uint32_t* total) {
+  constexpr int kWarps = kSelThreads / 32;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -49,24 +51,37 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_tot, u
   __syncthreads();                         // warp_tot of the previous scan has been read
   if (lane == 31) warp_tot[wid] = x;
   __syncthreads();
-  uint32_t t = warp_tot[lane];
+  uint32_t t = lane < kWarps ? warp_tot[lane] : 0u;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
+  for (int o = 1; o < kWarps; o <<= 1) {
     const uint32_t y = __shfl_up_sync(0xffffffffu, t, o);
     if (lane >= o) t += y;
   }
-  *total = __shfl_sync(0xffffffffu, t, 31);
+  *total = __shfl_sync(0xffffffffu, t, kWarps - 1);
   const uint32_t before = __shfl_sync(0xffffffffu, t, (wid + 31) & 31);
   return x + (wid ? before : 0u);
 }
 
-__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictProblem p, int cap) {
+// Counts digit d of the lanes for which `in` holds. Where one digit prevails (equal weights, zeros)
+// its lanes are counted with one addition; the rest add for themselves.
+__device__ __forceinline__ void count_digit(uint32_t* hist, uint32_t d, bool in) {
+  const uint32_t live = __ballot_sync(0xffffffffu, in);
+  if (live == 0) return;
+  const int first = __ffs(live) - 1;
+  const uint32_t d0 = __shfl_sync(0xffffffffu, d, first);
+  const uint32_t same = __ballot_sync(0xffffffffu, in && d == d0);
+  if (in && d != d0) atomicAdd(hist + d, 1u);
+  if ((threadIdx.x & 31) == first) atomicAdd(hist + d0, (uint32_t)__popc(same));
+}
+
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictProblem p, int cap) {
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  __shared__ uint32_t hist[3][kBins];
+  __shared__ __align__(16) uint32_t hist[3][kBins];
   __shared__ uint32_t warp_tot[32];
   __shared__ uint32_t s_bin, s_above;      // digit of the wanted key, keys above that digit
-  extern __shared__ uint32_t s_key[];      // [cap] this CTA's keys (when they fit)
+  __shared__ uint32_t s_keep[kSelThreads]; // which keys of a tile stay, a byte of bits per thread
+  extern __shared__ __align__(16) uint32_t s_key[];   // [cap] this CTA's keys (when they fit)
   const int tid = threadIdx.x;
   const int bh = blockIdx.x / C, b = bh / p.Hkv;
   for (int i = tid; i < 3 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
@@ -94,10 +109,21 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictProbl
   // This CTA's keys [j0, j1).
   const int part = min(((n + C - 1) / C + 3) & ~3, p.part);
   const int j0 = min(rank * part, n), j1 = min(j0 + part, n);
-  auto key_at = [&](int j) -> uint32_t {
-    const int at = pos ? pos[j] : j;
-    if (at < p.sink || (long long)at >= next - p.recent) return 0xFFFFFFFFu;
-    return rank_of(w[j]);
+  auto key_of = [&](int at, float weight) -> uint32_t {
+    return at < p.sink || (long long)at >= next - p.recent ? 0xFFFFFFFFu : rank_of(weight);
+  };
+  // Keys t0 + tid + i * kSelThreads, all loads in flight together (0 past the end).
+  auto load_tile = [&](int t0, uint32_t (&k)[kSelKeys]) {
+    float x[kSelKeys];
+    int at[kSelKeys];
+#pragma unroll
+    for (int i = 0; i < kSelKeys; ++i) {
+      const int j = t0 + tid + i * kSelThreads;
+      x[i] = j < j1 ? w[j] : 0.f;
+      at[i] = pos && j < j1 ? pos[j] : j;
+    }
+#pragma unroll
+    for (int i = 0; i < kSelKeys; ++i) k[i] = key_of(at[i], x[i]);
   };
 
   uint32_t thr = 0, need_eq = 0, eq_before = 0;
@@ -112,46 +138,65 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictProbl
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const int bits = pass == 2 ? 10 : 11;
       const uint32_t mask = (1u << bits) - 1;
-      for (int j = j0 + tid; j - tid < j1; j += kSelThreads) {
-        bool in = j < j1;
-        uint32_t k = 0;
-        if (in) {
-          k = (pass > 0 && held) ? s_key[j - j0] : key_at(j);
-          if (pass == 0 && held) s_key[j - j0] = k;
-          if (pass > 0) in = (k >> (shift + bits)) == (thr >> (shift + bits));
+      for (int t0 = j0; t0 < j1; t0 += kSelTile) {
+        uint32_t k[kSelKeys];
+        if (pass > 0 && held) {
+#pragma unroll
+          for (int i = 0; i < kSelKeys; ++i) {
+            const int j = t0 + tid + i * kSelThreads;
+            k[i] = j < j1 ? s_key[j - j0] : 0u;
+          }
+        } else {
+          load_tile(t0, k);
+          if (held) {
+#pragma unroll
+            for (int i = 0; i < kSelKeys; ++i) {
+              const int j = t0 + tid + i * kSelThreads;
+              if (j < j1) s_key[j - j0] = k[i];
+            }
+          }
         }
-        // Weights share their leading bits: one addition per distinct digit of a warp.
-        const uint32_t live = __ballot_sync(0xffffffffu, in);
-        if (in) {
-          const uint32_t d = (k >> shift) & mask;
-          const uint32_t same = __match_any_sync(live, d);
-          if ((threadIdx.x & 31) == __ffs(same) - 1) atomicAdd(&hist[pass][d], (uint32_t)__popc(same));
+#pragma unroll
+        for (int i = 0; i < kSelKeys; ++i) {
+          bool in = t0 + tid + i * kSelThreads < j1;
+          if (pass > 0) in = in && (k[i] >> (shift + bits)) == (thr >> (shift + bits));
+          count_digit(hist[pass], (k[i] >> shift) & mask, in);
         }
       }
       cluster.sync();
       // Sum over the cluster, then the digit at which the count from the top reaches `want`.
-      // Thread t holds bins top - 2t and top - 2t - 1.
-      const int top = (int)mask - 2 * tid;
-      uint32_t c0 = 0, c1 = 0;
+      // Thread t holds the four bins from top - 4t down.
+      constexpr int kPer = kBins / kSelThreads;
+      static_assert(kPer == 4, "bins of a thread");
+      const int top = (int)mask - kPer * tid;
+      uint32_t c[kPer] = {0, 0, 0, 0};     // c[0]: the highest bin
       if (top > 0) {
-        uint2 v[kMaxEvictCtas];            // (all loads in flight together)
+        uint4 v[kMaxEvictCtas];            // (all loads in flight together)
 #pragma unroll
         for (int r = 0; r < kMaxEvictCtas; ++r)
-          v[r] = r < C ? *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&hist[pass][top - 1], r))
-                       : make_uint2(0u, 0u);
+          v[r] = r < C ? *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&hist[pass][top - 3], r))
+                       : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int r = 0; r < kMaxEvictCtas; ++r) {
-          c0 += v[r].y;
-          c1 += v[r].x;
+          c[0] += v[r].w;
+          c[1] += v[r].z;
+          c[2] += v[r].y;
+          c[3] += v[r].x;
         }
       }
       uint32_t total;
-      const uint32_t incl = block_scan(c0 + c1, warp_tot, &total);
-      const uint32_t excl = incl - c0 - c1;
-      if (top > 0 && excl < want && want <= incl) {
-        const bool first = want <= excl + c0;
-        s_bin = (uint32_t)(first ? top : top - 1);
-        s_above = first ? excl : excl + c0;
+      const uint32_t sum = c[0] + c[1] + c[2] + c[3];
+      const uint32_t incl = block_scan(sum, warp_tot, &total);
+      uint32_t above = incl - sum;
+      if (above < want && want <= incl) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          if (above < want && want <= above + c[i]) {
+            s_bin = (uint32_t)(top - i);
+            s_above = above;
+          }
+          above += c[i];
+        }
       }
       __syncthreads();
       thr |= s_bin << shift;
@@ -160,9 +205,9 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictProbl
         const uint32_t d = thr & mask;
         uint32_t all = 0;
         for (int r = 0; r < C; ++r) {
-          const uint32_t c = *cluster.map_shared_rank(&hist[2][d], r);
-          if (r < rank) eq_before += c;
-          all += c;
+          const uint32_t x = *cluster.map_shared_rank(&hist[2][d], r);
+          if (r < rank) eq_before += x;
+          all += x;
         }
         need_eq = want;
         all_eq = need_eq == all;
@@ -174,68 +219,60 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictProbl
   const bool copy_pos = pos_out && p.key_pos_out != p.key_pos;
   uint32_t n_holes = 0, n_movers = 0;
   for (int t0 = j0; t0 < j1; t0 += kSelTile) {
-    const int j = t0 + 4 * tid;
-    uint32_t k[4] = {0, 0, 0, 0};
-    uint32_t keep = 0;                     // bit e: key j + e stays
+    const int j = t0 + kSelKeys * tid;     // this thread's run of keys
+    const int cnt = max(0, min(kSelKeys, j1 - j));
+    uint32_t keep = (1u << cnt) - 1;       // bit e: key j + e stays
     if (evicts) {
-      uint32_t eq = 0;
+      uint32_t above = 0, eq = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (j + e < j1) {
-          k[e] = held ? s_key[j + e - j0] : key_at(j + e);
-          if (k[e] > thr) keep |= 1u << e;
-          if (k[e] == thr) eq |= 1u << e;
+      for (int e = 0; e < kSelKeys; ++e) {
+        if (e < cnt) {
+          const uint32_t k = held ? s_key[j + e - j0] : key_of(pos ? pos[j + e] : j + e, w[j + e]);
+          above |= (uint32_t)(k > thr) << e;
+          eq |= (uint32_t)(k == thr) << e;
         }
       }
-      if (all_eq) {
-        keep |= eq;
-      } else {                             // the lowest slots among equals
+      keep = above | eq;
+      if (!all_eq) {                       // the lowest slots among equals
         uint32_t total;
-        uint32_t at = eq_before + block_scan(__popc(eq), warp_tot, &total) - __popc(eq);
+        const uint32_t at = eq_before + block_scan(__popc(eq), warp_tot, &total) - __popc(eq);
         eq_before += total;
+        uint32_t left = need_eq > at ? need_eq - at : 0u;
+        keep = above;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (eq >> e & 1) {
-            if (at < need_eq) keep |= 1u << e;
-            ++at;
+        for (int e = 0; e < kSelKeys; ++e) {
+          if ((eq >> e & 1) && left > 0) {
+            keep |= 1u << e;
+            --left;
           }
         }
       }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (j + e < j1) keep |= 1u << e;
-    }
-    uint32_t hole = 0, mover = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int s = j + e;
-      if (s >= j1) continue;
-      if (s < Lk) {
-        if (keep >> e & 1) {
-          if (copy_w) w_out[s] = w[s];
-          if (copy_pos) pos_out[s] = pos ? pos[s] : s;
-          if (kept) kept[s] = s;
-        } else {
-          hole |= 1u << e;
-        }
-      } else if (keep >> e & 1) {
-        mover |= 1u << e;
-      }
-    }
-    if (evicts) {
+      const int low = max(0, min(kSelKeys, Lk - j));   // keys of the run below the new length
+      const uint32_t below = (1u << low) - 1;
+      uint32_t hole = ~keep & below & ((1u << cnt) - 1), mover = keep & ~below;
       uint32_t total;                      // two counts of at most kSelTile in one word
-      const uint32_t cnt = __popc(hole) | __popc(mover) << 16;
-      const uint32_t at = block_scan(cnt, warp_tot, &total) - cnt;
-      uint32_t ah = n_holes + (at & 0xFFFFu), am = n_movers + (at >> 16);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (hole >> e & 1) holes[ah++] = j + e;
-        if (mover >> e & 1) movers[am++] = j + e;
-      }
+      const uint32_t both = __popc(hole) | __popc(mover) << 16;
+      const uint32_t at = block_scan(both, warp_tot, &total) - both;
+      int* hp = holes + n_holes + (at & 0xFFFFu);
+      int* mp = movers + n_movers + (at >> 16);
+      for (; hole; hole &= hole - 1) *hp++ = j + __ffs(hole) - 1;
+      for (; mover; mover &= mover - 1) *mp++ = j + __ffs(mover) - 1;
       n_holes += total & 0xFFFFu;
       n_movers += total >> 16;
     }
+    // What stays in place, consecutive threads on consecutive slots.
+    s_keep[tid] = keep;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSelKeys; ++i) {
+      const int x = tid + i * kSelThreads, s = t0 + x;
+      if (s < min(j1, Lk) && (s_keep[x / kSelKeys] >> (x % kSelKeys) & 1)) {
+        if (copy_w) w_out[s] = w[s];
+        if (copy_pos) pos_out[s] = pos ? pos[s] : s;
+        if (kept) kept[s] = s;
+      }
+    }
+    __syncthreads();
   }
   if (tid == 0) {
     list->holes = (int)n_holes;
@@ -258,7 +295,7 @@ __device__ __forceinline__ int list_at(const int* slots, const int* ends, int C,
   return slots[((size_t)r * 2 + which) * part + (k - before)];
 }
 
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictProblem p, int C) {
+__global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(EvictProblem p, int C) {
   __shared__ int s_holes[kMaxEvictCtas], s_movers[kMaxEvictCtas];
   const int bh = blockIdx.y, b = bh / p.Hkv, h = bh - b * p.Hkv;
   pdl_trigger();
@@ -286,39 +323,47 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictProblem p
     if (page < 0 || page >= p.num_pages) return -1;
     return (((long long)page * p.Hkv + h) * p.page_size + slot % p.page_size) * (kHeadDim / 8);
   };
-  const int warps = gridDim.x * (kMoveThreads / 32);
-  for (int k0 = (blockIdx.x * (kMoveThreads / 32) + warp) * kMoveRows; k0 < moves; k0 += warps * kMoveRows) {
-    // Lane l < kMoveRows looks up move k0 + l, and moves its weight and position.
-    int to = 0, from = 0;
-    long long rt = -1, rf = -1;
+  const int stride = gridDim.x * (kMoveThreads / 32) * kMoveRows;
+  // Lane l < kMoveRows looks up move k0 + l (one turn ahead of the rows' copies).
+  auto look_up = [&](int k0, int& to, int& from) {
+    to = from = -1;
     if (lane < kMoveRows && k0 + lane < moves) {
       to = list_at(slots, s_holes, C, p.part, 0, k0 + lane);
       from = list_at(slots, s_movers, C, p.part, 1, k0 + lane);
-      rt = row(to);
-      rf = row(from);
-      w_out[to] = w[from];
-      if (p.key_pos_out)
-        p.key_pos_out[(size_t)bh * p.S + to] = p.key_pos ? p.key_pos[(size_t)bh * p.S + from] : from;
-      if (p.kept_slots) p.kept_slots[(size_t)bh * p.budget + to] = from;
     }
+  };
+  int k0 = (blockIdx.x * (kMoveThreads / 32) + warp) * kMoveRows;
+  int to, from, next_to, next_from;
+  look_up(k0, to, from);
+  for (; k0 < moves; k0 += stride) {
+    const long long rt = to >= 0 ? row(to) : -1, rf = from >= 0 ? row(from) : -1;
     uint4 v[kMoveRows];
 #pragma unroll
     for (int i = 0; i < kMoveRows; ++i) {
       const long long f = __shfl_sync(0xffffffffu, rf, i);
       if (f >= 0) v[i] = __ldcs(cache + f);
     }
+    look_up(k0 + stride, next_to, next_from);
+    if (to >= 0) {                          // the lane's own move: weight and position
+      w_out[to] = w[from];
+      if (p.key_pos_out)
+        p.key_pos_out[(size_t)bh * p.S + to] = p.key_pos ? p.key_pos[(size_t)bh * p.S + from] : from;
+      if (p.kept_slots) p.kept_slots[(size_t)bh * p.budget + to] = from;
+    }
 #pragma unroll
     for (int i = 0; i < kMoveRows; ++i) {
       const long long f = __shfl_sync(0xffffffffu, rf, i), t = __shfl_sync(0xffffffffu, rt, i);
       if (f >= 0 && t >= 0) cache[t] = v[i];
     }
+    to = next_to;
+    from = next_from;
   }
 }
 
 }  // namespace
 
 int evict_ctas(int S) {
-  // One CTA per 4096 keys of capacity (four keys a thread), at most a portable cluster.
+  // One CTA per 4096 keys of capacity (eight keys a thread), at most a portable cluster.
   int c = 1;
   while (c < kMaxEvictCtas && c * kSelTile < S) c *= 2;
   return c;

@@ -22,7 +22,8 @@ namespace la {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kItems = 4;        // items whose loads a thread keeps in flight
+// Items whose loads a thread keeps in flight: 128 bytes, with registers for four blocks an SM.
+template <typename E> constexpr int kItemsOf = sizeof(E) == 4 ? 2 : 4;
 
 template <typename E> struct Vec8;
 template <> struct Vec8<float> {
@@ -159,9 +160,10 @@ __device__ __forceinline__ bool item_chunks(int s, int pairs, int* ca, int* cb) 
 
 // ---- Rotation alone: `tok` tokens per block.
 template <typename E, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, 4)
     rope_kernel(const __grid_constant__ la_rope_plan pl, RopeProblem p, int tok) {
   extern __shared__ float2 s_cs[];      // [tok][pairs]
+  constexpr int kItems = kItemsOf<E>;
   pdl_trigger();
   pdl_wait();
   const int pairs = pl.rotary_dim >> 1;
@@ -247,7 +249,7 @@ __global__ void __launch_bounds__(kRopeThreads)
 
 // ---- Rotation and append. Row (b, i) of a padded batch of T rows a sequence: q rotated into
 // q_out, k rotated into the cache slot P_b + i, v copied there, its position into key_pos.
-constexpr int kAppendTok = 8;           // most tokens per block
+constexpr int kAppendTok = 16;          // most tokens per block
 
 struct TokenAt {
   long long row;                        // cache row of KV head 0, or -1: nothing is appended
@@ -257,9 +259,10 @@ struct TokenAt {
 };
 
 template <bool HALF, bool SCALAR>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, 4)
     rope_append_kernel(const __grid_constant__ la_rope_plan pl, RopeAppendProblem p, int tok) {
   using E = __nv_bfloat16;
+  constexpr int kItems = kItemsOf<E>;
   __shared__ float2 s_cs[kAppendTok * kHeadDim / 2];
   __shared__ TokenAt s_at[kAppendTok];
   pdl_trigger();
@@ -389,7 +392,7 @@ cudaError_t launch_rope_t(const la_rope_plan& pl, const RopeProblem& p, bool vec
   // Tokens per block: a full set of loads for every thread, at most 32 KB of cosines and sines, and
   // (few tokens) no more than spreads them over two blocks per SM.
   const int per_tok = p.heads * (vec ? p.head_dim / 16 : p.head_dim / 2);
-  long long tok = (long long)kRopeThreads * kItems / (per_tok > 0 ? per_tok : 1);
+  long long tok = (long long)kRopeThreads * kItemsOf<E> / per_tok;
   if (tok > 4096 / pairs) tok = 4096 / pairs;
   if (tok > p.tokens / 296) tok = p.tokens / 296;
   if (tok < 1) tok = 1;
@@ -421,9 +424,11 @@ cudaError_t launch_rope(const la_rope_plan& pl, const RopeProblem& p, int dtype,
 
 cudaError_t launch_rope_append(const la_rope_plan& pl, const RopeAppendProblem& p, cudaStream_t s) {
   const long long tokens = (long long)p.B * p.T;
-  // Tokens per block: few tokens are spread over the SMs, many share a block's angles.
-  long long tok = tokens / 296;
+  // Tokens per block: one full set of loads for every thread (6 at 16 + 2 + 2 heads), and few tokens
+  // spread over two blocks per SM.
+  long long tok = kRopeThreads * kItemsOf<__nv_bfloat16> / ((p.Hq + 2LL * p.Hkv) * (kHeadDim / 16));
   if (tok > kAppendTok) tok = kAppendTok;
+  if (tok > tokens / 296) tok = tokens / 296;
   if (tok < 1) tok = 1;
   const dim3 grid((unsigned)((tokens + tok - 1) / tok));
   const bool half = pl.layout == LA_ROPE_HALF;

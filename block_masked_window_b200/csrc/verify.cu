@@ -14,7 +14,7 @@
 // Bound: memory, one row of p and one of q per sequence, read once. A cluster of C CTAs shares a
 // sequence: each warp sums one contiguous range of the row (loads coalesced, 8 + 8 in flight
 // a lane), the ranges' sums meet through distributed shared memory, and the CTA that owns the range
-// in which the draw falls goes over that range alone again (1/(32 C) of the row, from L2).
+// in which the draw falls goes over that range alone again (1/(16 C) of the row, from L2).
 #include <cooperative_groups.h>
 
 #include "pbd_common.cuh"
@@ -25,7 +25,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kVThreads = 1024;
+constexpr int kVThreads = 512;
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kVMaxCtas = 8;
 constexpr int kVUnroll = 8;
@@ -120,16 +120,19 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyProblem a) {
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) s_sum[attempt][warp] = sum;
     cluster.sync();
-    // Every CTA finds the draw's range among the C * 32 ranges (lane l of warp 0: C of them).
+    // Every CTA finds the draw's range among the C * kVWarps ranges (lane l of warp 0: `of_lane`).
     if (warp == 0) {
-      double part[kVMaxCtas], mine = 0.0;
+      constexpr int kPart = kVMaxCtas * kVWarps / 32;
+      const int of_lane = (C * kVWarps + 31) / 32;
+      double part[kPart], mine = 0.0;
 #pragma unroll
-      for (int i = 0; i < kVMaxCtas; ++i) {
-        const int r = lane * C + i;
-        part[i] = i < C ? *cluster.map_shared_rank(&s_sum[attempt][r % kVWarps], r / kVWarps) : 0.0;
+      for (int i = 0; i < kPart; ++i) {
+        const int r = lane * of_lane + i;
+        part[i] = i < of_lane && r < C * kVWarps
+                      ? *cluster.map_shared_rank(&s_sum[attempt][r % kVWarps], r / kVWarps) : 0.0;
       }
 #pragma unroll
-      for (int i = 0; i < kVMaxCtas; ++i) mine += part[i];
+      for (int i = 0; i < kPart; ++i) mine += part[i];
       double incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -141,12 +144,12 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyProblem a) {
       double run = incl - mine, before = 0.0, before_last = 0.0;
       int range = -1, range_last = -1;     // first range that passes the goal; last with any weight
 #pragma unroll
-      for (int i = 0; i < kVMaxCtas; ++i) {
-        if (i < C && part[i] > 0.0) {
-          range_last = lane * C + i;
+      for (int i = 0; i < kPart; ++i) {
+        if (part[i] > 0.0) {
+          range_last = lane * of_lane + i;
           before_last = run;
           if (range < 0 && run + part[i] > goal) {
-            range = lane * C + i;
+            range = lane * of_lane + i;
             before = run;
           }
           run += part[i];
