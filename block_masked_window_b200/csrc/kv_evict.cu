@@ -204,10 +204,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictProbl
       if (pass == 2) {
         const uint32_t d = thr & mask;
         uint32_t all = 0;
-        for (int r = 0; r < C; ++r) {
-          const uint32_t x = *cluster.map_shared_rank(&hist[2][d], r);
-          if (r < rank) eq_before += x;
-          all += x;
+        uint32_t x[kMaxEvictCtas];
+#pragma unroll
+        for (int r = 0; r < kMaxEvictCtas; ++r) x[r] = r < C ? *cluster.map_shared_rank(&hist[2][d], r) : 0u;
+#pragma unroll
+        for (int r = 0; r < kMaxEvictCtas; ++r) {
+          if (r < rank) eq_before += x[r];
+          all += x[r];
         }
         need_eq = want;
         all_eq = need_eq == all;
@@ -263,12 +266,24 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictProbl
     // What stays in place, consecutive threads on consecutive slots.
     s_keep[tid] = keep;
     __syncthreads();
+    float wv[kSelKeys];
+    int pv[kSelKeys];
+    uint32_t in_place = 0;
 #pragma unroll
-    for (int i = 0; i < kSelKeys; ++i) {
+    for (int i = 0; i < kSelKeys; ++i) {   // (all loads in flight before the stores)
       const int x = tid + i * kSelThreads, s = t0 + x;
       if (s < min(j1, Lk) && (s_keep[x / kSelKeys] >> (x % kSelKeys) & 1)) {
-        if (copy_w) w_out[s] = w[s];
-        if (copy_pos) pos_out[s] = pos ? pos[s] : s;
+        in_place |= 1u << i;
+        if (copy_w) wv[i] = w[s];
+        pv[i] = copy_pos && pos ? pos[s] : s;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kSelKeys; ++i) {
+      const int s = t0 + tid + i * kSelThreads;
+      if (in_place >> i & 1) {
+        if (copy_w) w_out[s] = wv[i];
+        if (copy_pos) pos_out[s] = pv[i];
         if (kept) kept[s] = s;
       }
     }
@@ -283,7 +298,8 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictProbl
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 8;               // keys a warp keeps in flight
+constexpr int kMoveRows = 4;               // keys a warp keeps in flight
+constexpr int kMoveCtas = 6;               // blocks per SM
 
 // Slot k of a list that is spread over the parts of C CTAs.
 __device__ __forceinline__ int list_at(const int* slots, const int* ends, int C, int part, int which, int k) {
@@ -295,7 +311,7 @@ __device__ __forceinline__ int list_at(const int* slots, const int* ends, int C,
   return slots[((size_t)r * 2 + which) * part + (k - before)];
 }
 
-__global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(EvictProblem p, int C) {
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtas) evict_move_kernel(EvictProblem p, int C) {
   __shared__ int s_holes[kMaxEvictCtas], s_movers[kMaxEvictCtas];
   const int bh = blockIdx.y, b = bh / p.Hkv, h = bh - b * p.Hkv;
   pdl_trigger();
@@ -396,12 +412,12 @@ cudaError_t launch_evict(const EvictProblem& p, int sms, cudaStream_t s) {
   e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, cap);
   if (e != cudaSuccess) return e;
   // Blocks per (sequence, KV head): enough for every possible move, but together no more than
-  // fill the GPU (a block then takes several turns).
+  // are resident at once (a block then takes several turns: one wave, evenly filled).
   const int heads = p.B * p.Hkv;
   const long long most = p.budget < p.S - p.budget ? p.budget : p.S - p.budget;
   const int per_block = kMoveThreads / 32 * kMoveRows;
   long long x = (most + per_block - 1) / per_block;
-  const long long fill = (8LL * sms + heads - 1) / heads;
+  const long long fill = (long long)kMoveCtas * sms / heads;
   if (x > fill) x = fill;
   if (x < 1) x = 1;
   return launch_pdl(evict_move_kernel, dim3((unsigned)x, (unsigned)heads), dim3(kMoveThreads), 0, s, p, C);

@@ -149,7 +149,7 @@ la_status rope_append(const la_pbd_cfg* cfg, const la_rope_plan* plan, const voi
   la_status st = check_plan(plan, la::kHeadDim);
   if (st != LA_OK) return st;
   if (rows < 1) return LA_ERR_INVALID_ARG;
-  if ((long long)cfg->batch * rows >= (1LL << 31)) return LA_ERR_UNSUPPORTED;
+  if ((long long)cfg->batch * rows >= (1LL << 30)) return LA_ERR_UNSUPPORTED;
   if (!q || !k_new || !v_new || !q_out || !kc || !vc) return LA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(q_out, 16) ||
       !aligned(kc, 16) || !aligned(vc, 16) || !aligned(seq_lens, 4) || !aligned(row_lens, 4) ||
@@ -184,7 +184,9 @@ la_status rope_append(const la_pbd_cfg* cfg, const la_rope_plan* plan, const voi
   p.Hq = cfg->num_q_heads;
   p.Hkv = cfg->num_kv_heads;
   p.S = pg.block_table ? pg.pages_per_seq * pg.page_size : cfg->max_seq;
-  return la::launch_rope_append(*plan, p, (cudaStream_t)stream) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+  int sms = 0;
+  if (la::sm_count(&sms) != cudaSuccess) return LA_ERR_CUDA;
+  return la::launch_rope_append(*plan, p, sms, (cudaStream_t)stream) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 
 // Workspace of la_kv_evict: header, list heads, lists.

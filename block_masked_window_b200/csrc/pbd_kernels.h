@@ -90,7 +90,8 @@ struct RopeAppendProblem {
   int pages_per_seq, page_size, num_pages;
   int B, T, Hq, Hkv, S;         // S = key slots of a sequence
 };
-cudaError_t launch_rope_append(const la_rope_plan& plan, const RopeAppendProblem& p, cudaStream_t stream);
+cudaError_t launch_rope_append(const la_rope_plan& plan, const RopeAppendProblem& p, int sms,
+                               cudaStream_t stream);
 
 // Eviction: see kv_evict.cu.
 constexpr int kMaxEvictCtas = 8;

@@ -93,45 +93,60 @@ __device__ __forceinline__ void from_f32(float* d, float x) { *d = x; }
 __device__ __forceinline__ void from_f32(__nv_bfloat16* d, float x) { *d = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void from_f32(__half* d, float x) { *d = __float2half_rn(x); }
 
-// (scaled cosine, scaled sine) of pair i at position t.
-__device__ __forceinline__ float2 turn_of(const la_rope_plan& pl, int i, long long t, float sign) {
-  const double turns = (double)t * pl.turns[i];
+// (scaled cosine, scaled sine) at position t of a pair that makes f turns per position.
+__device__ __forceinline__ float2 turn_at(double f, float scale, long long t) {
+  const double turns = (double)t * f;
   const float x = (float)(2.0 * (turns - rint(turns)));   // half turns in [-1, 1]
   float s, c;
   sincospif(x, &s, &c);
-  return make_float2(c * pl.out_scale, s * pl.out_scale * sign);
+  return make_float2(c * scale, s * scale);
+}
+__device__ __forceinline__ float2 turn_of(const la_rope_plan& pl, int i, long long t, float sign) {
+  float2 c = turn_at(pl.turns[i], pl.out_scale, t);
+  c.y *= sign;
+  return c;
 }
 
-// Rotates the 16 channels of one item. cs: the token's (cos, sin) pairs. Half layout: a and b
-// hold the first and second halves of pairs i0 .. i0 + 7. Interleaved: a and b hold pairs
-// i0 .. i0 + 3 and i0 + 4 .. i0 + 7; pairs from `pairs` on are copied.
+// Cosines and sines of a token are kept as two pairs to a float4, pairs 8s + 2e, 8s + 2e + 1 of
+// item s at [e][s]: neighbouring items (lanes) then read neighbouring 16-byte words.
+__device__ __forceinline__ int table_at(int pair, int rot) {   // rot = items that hold pairs
+  const int s = pair >> 3, e = (pair & 7) >> 1;
+  return 2 * (e * rot + s) + (pair & 1);                       // in float2
+}
+struct Turn8 {
+  float4 cs[4];                                                // (cos, sin) of pairs 2e and 2e + 1
+  __device__ __forceinline__ void load(const float2* table, int s, int rot) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) cs[e] = reinterpret_cast<const float4*>(table)[e * rot + s];
+  }
+  __device__ __forceinline__ float cos_of(int e) const { return (e & 1) ? cs[e >> 1].z : cs[e >> 1].x; }
+  __device__ __forceinline__ float sin_of(int e) const { return (e & 1) ? cs[e >> 1].w : cs[e >> 1].y; }
+};
+
+// Rotates the 16 channels of one item, pairs i0 .. i0 + 7. Half layout: a and b hold the pairs'
+// first and second channels. Interleaved: a holds pairs i0 .. i0 + 3 and b the next four;
+// pairs from `pairs` on are copied.
 template <bool HALF, typename E>
-__device__ __forceinline__ void rotate_item(Vec8<E>& a, Vec8<E>& b, const float2* cs, int i0, int pairs) {
+__device__ __forceinline__ void rotate_item(Vec8<E>& a, Vec8<E>& b, const Turn8& t, int i0, int pairs) {
   float x[8], y[8];
   a.get(x);
   b.get(y);
   if (HALF) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float2 c = cs[i0 + e];
-      const float u = x[e], w = y[e];
-      x[e] = fmaf(u, c.x, -(w * c.y));
-      y[e] = fmaf(w, c.x, u * c.y);
+      const float c = t.cos_of(e), s = t.sin_of(e), u = x[e], w = y[e];
+      x[e] = fmaf(u, c, -(w * s));
+      y[e] = fmaf(w, c, u * s);
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 8; ++e) {
+      float* z = e < 4 ? x : y;
+      const int k = 2 * (e & 3);
       if (i0 + e < pairs) {
-        const float2 c = cs[i0 + e];
-        const float u = x[2 * e], w = x[2 * e + 1];
-        x[2 * e] = fmaf(u, c.x, -(w * c.y));
-        x[2 * e + 1] = fmaf(w, c.x, u * c.y);
-      }
-      if (i0 + 4 + e < pairs) {
-        const float2 c = cs[i0 + 4 + e];
-        const float u = y[2 * e], w = y[2 * e + 1];
-        y[2 * e] = fmaf(u, c.x, -(w * c.y));
-        y[2 * e + 1] = fmaf(w, c.x, u * c.y);
+        const float c = t.cos_of(e), s = t.sin_of(e), u = z[k], w = z[k + 1];
+        z[k] = fmaf(u, c, -(w * s));
+        z[k + 1] = fmaf(w, c, u * s);
       }
     }
   }
@@ -162,11 +177,11 @@ __device__ __forceinline__ bool item_chunks(int s, int pairs, int* ca, int* cb) 
 template <typename E, bool HALF>
 __global__ void __launch_bounds__(kRopeThreads, 4)
     rope_kernel(const __grid_constant__ la_rope_plan pl, RopeProblem p, int tok) {
-  extern __shared__ float2 s_cs[];      // [tok][pairs]
+  extern __shared__ __align__(16) float2 s_cs[];   // [tok][8 rot], see table_at
   constexpr int kItems = kItemsOf<E>;
   pdl_trigger();
   pdl_wait();
-  const int pairs = pl.rotary_dim >> 1;
+  const int pairs = pl.rotary_dim >> 1, rot = (pairs + 7) >> 3;
   const long long t0 = (long long)blockIdx.x * tok;
   const int nt = (int)min((long long)tok, p.tokens - t0);
   const int ns = p.head_dim >> 4;
@@ -190,8 +205,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
     }
     if (base == threadIdx.x) {          // (first pass, every thread)
       for (int i = threadIdx.x; i < nt * pairs; i += kRopeThreads) {
-        const int t = i / pairs;
-        s_cs[i] = turn_of(pl, i - t * pairs, __ldg(p.positions + t0 + t), p.sign);
+        const int t = i / pairs, pair = i - t * pairs;
+        s_cs[t * 8 * rot + table_at(pair, rot)] = turn_of(pl, pair, __ldg(p.positions + t0 + t), p.sign);
       }
       __syncthreads();
     }
@@ -201,8 +216,11 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
       if (it < total) {
         const int t = it / per_tok, rem = it - t * per_tok, h = rem / ns, s = rem - h * ns;
         int ca, cb;
-        if (item_chunks<HALF>(s, pairs, &ca, &cb))
-          rotate_item<HALF>(a[k], b[k], s_cs + t * pairs, 8 * s, pairs);
+        if (item_chunks<HALF>(s, pairs, &ca, &cb)) {
+          Turn8 turn;
+          turn.load(s_cs + t * 8 * rot, s, rot);
+          rotate_item<HALF>(a[k], b[k], turn, 8 * s, pairs);
+        }
         E* dst = y + (t0 + t) * p.y_tok + h * p.y_head;
         a[k].store(dst + ca);
         b[k].store(dst + cb);
@@ -249,138 +267,117 @@ __global__ void __launch_bounds__(kRopeThreads)
 
 // ---- Rotation and append. Row (b, i) of a padded batch of T rows a sequence: q rotated into
 // q_out, k rotated into the cache slot P_b + i, v copied there, its position into key_pos.
-constexpr int kAppendTok = 16;          // most tokens per block
-
-struct TokenAt {
-  long long row;                        // cache row of KV head 0, or -1: nothing is appended
-  long long tok;                        // row of q, k_new, v_new and q_out, or -1: padding
-  long long pos;
-  int b, slot;
-};
+//
+// One warp per token (warps stride over the tokens): lane l holds channels of item l % 8 of heads
+// l / 8, l / 8 + 4, ..., so that the 8 pairs it turns are the same for all of them. The lanes
+// compute two pairs' cosines and sines each, exchange them through the warp's shared memory, and
+// keep their eight in registers. No barrier of the block, no division per item.
+constexpr int kAppendWarps = 4;         // per block
+constexpr int kAppendItems = 5;         // heads a lane keeps in flight (16 + 2 + 2 heads: all of them)
 
 template <bool HALF, bool SCALAR>
-__global__ void __launch_bounds__(kRopeThreads, 4)
-    rope_append_kernel(const __grid_constant__ la_rope_plan pl, RopeAppendProblem p, int tok) {
+__global__ void __launch_bounds__(32 * kAppendWarps, 6)
+    rope_append_kernel(const __grid_constant__ la_rope_plan pl, RopeAppendProblem p) {
   using E = __nv_bfloat16;
-  constexpr int kItems = kItemsOf<E>;
-  __shared__ float2 s_cs[kAppendTok * kHeadDim / 2];
-  __shared__ TokenAt s_at[kAppendTok];
+  __shared__ __align__(16) float2 s_cs[kAppendWarps][kHeadDim / 2];
   pdl_trigger();
-  pdl_wait();
-  const int pairs = pl.rotary_dim >> 1;
-  const long long t0 = (long long)blockIdx.x * tok;
-  const int nt = (int)min((long long)tok, (long long)p.B * p.T - t0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float2* table = s_cs[warp];
+  const int pairs = pl.rotary_dim >> 1, rot = (pairs + 7) >> 3;
+  const double f0 = lane < pairs ? pl.turns[lane] : 0.0, f1 = lane + 32 < pairs ? pl.turns[lane + 32] : 0.0;
   const int heads = p.Hq + 2 * p.Hkv;
-  if (threadIdx.x < nt) {
-    const long long t = t0 + threadIdx.x;
-    const int b = (int)(t / p.T), i = (int)(t - (long long)b * p.T);
-    const int P = p.seq_lens ? __ldg(p.seq_lens + b) : 0;
-    const int w = p.row_lens ? __ldg(p.row_lens + b) : p.T;
-    const int at = p.pos0 ? __ldg(p.pos0 + b) : P;
-    TokenAt a;
-    a.b = b;
-    a.pos = (long long)at + i;
-    a.slot = P + i;
-    a.tok = t;
-    a.row = -1;
-    if (P < 0 || w < 0 || w > p.T || (long long)P + w > p.S || i >= w) {
-      a.tok = -1;                       // padding, or a sequence whose lengths are invalid
-    } else if (p.block_table) {
-      const int page = __ldg(p.block_table + (size_t)b * p.pages_per_seq + a.slot / p.page_size);
-      if (page >= 0 && page < p.num_pages)
-        a.row = (long long)page * p.Hkv * p.page_size + a.slot % p.page_size;
-    } else {
-      a.row = (long long)b * p.Hkv * p.S + a.slot;
-    }
-    s_at[threadIdx.x] = a;
-  }
-  // Row r of the block: (token r / heads, head r % heads; q heads, then k, then v).
-  auto source = [&](int t, int h) -> const E* {
-    const long long row = t0 + t;
-    if (h < p.Hq) return p.q + row * p.q_tok + (long long)h * kHeadDim;
-    h -= p.Hq;
-    if (h < p.Hkv) return p.k_new + row * p.k_tok + (long long)h * kHeadDim;
-    return p.v_new + row * p.v_tok + (long long)(h - p.Hkv) * kHeadDim;
-  };
-  auto target = [&](const TokenAt& a, int h) -> E* {   // null: not written
-    if (a.tok < 0) return nullptr;
-    if (h < p.Hq) return p.q_out + (a.tok * p.Hq + h) * kHeadDim;
-    if (a.row < 0) return nullptr;
-    h -= p.Hq;
-    const int hk = h < p.Hkv ? h : h - p.Hkv;
-    const long long row = a.row + (long long)hk * (p.block_table ? p.page_size : p.S);
-    return (h < p.Hkv ? p.kc : p.vc) + row * kHeadDim;
-  };
-  auto angles = [&]() {
-    __syncthreads();                    // s_at
-    for (int i = threadIdx.x; i < nt * pairs; i += kRopeThreads) {
-      const int t = i / pairs;
-      if (s_at[t].tok >= 0) s_cs[i] = turn_of(pl, i - t * pairs, s_at[t].pos, 1.f);
-    }
-    if (p.key_pos) {
-      for (int i = threadIdx.x; i < nt * p.Hkv; i += kRopeThreads) {
-        const TokenAt a = s_at[i / p.Hkv];
-        if (a.row >= 0)
-          p.key_pos[((size_t)a.b * p.Hkv + i % p.Hkv) * p.S + a.slot] = (int)a.pos;
-      }
-    }
-    __syncthreads();
-  };
-  if (SCALAR) {
-    angles();
-    const int total = nt * heads * (kHeadDim / 2);
-    for (int it = threadIdx.x; it < total; it += kRopeThreads) {
-      const int i = it % (kHeadDim / 2), r = it / (kHeadDim / 2), t = r / heads, h = r - t * heads;
-      E* dst = target(s_at[t], h);
-      if (!dst) continue;
-      const E* src = source(t, h);
-      const bool rot = i < pairs && h < p.Hq + p.Hkv;
-      const int ca = (HALF && i < pairs) ? i : 2 * i, cb = (HALF && i < pairs) ? i + pairs : 2 * i + 1;
-      const E xa = src[ca], xb = src[cb];
-      if (rot) {
-        const float2 c = s_cs[t * pairs + i];
-        const float u = to_f32(xa), w = to_f32(xb);
-        dst[ca] = __float2bfloat16_rn(fmaf(u, c.x, -(w * c.y)));
-        dst[cb] = __float2bfloat16_rn(fmaf(w, c.x, u * c.y));
-      } else {
-        dst[ca] = xa;
-        dst[cb] = xb;
-      }
-    }
-    return;
-  }
-  constexpr int kNs = kHeadDim / 16;    // items of a head
-  const int s = threadIdx.x % kNs;
+  const int s = lane & 7, g = lane >> 3;
   int ca, cb;
-  const bool rot = item_chunks<HALF>(s, pairs, &ca, &cb);
-  const int rows = nt * heads;
-  bool first = true;
-  for (int r0 = threadIdx.x / kNs; first || r0 < rows; r0 += kRopeThreads / kNs * kItems) {
-    Vec8<E> a[kItems], b[kItems];
+  const bool turns = item_chunks<HALF>(s, pairs, &ca, &cb);
+  pdl_wait();
+  const int tokens = p.B * p.T, step = gridDim.x * kAppendWarps;
+  for (int tok = blockIdx.x * kAppendWarps + warp; tok < tokens; tok += step) {
+    const E* qs = p.q + (long long)tok * p.q_tok;
+    const E* ks = p.k_new + (long long)tok * p.k_tok;
+    const E* vs = p.v_new + (long long)tok * p.v_tok;
+    auto source = [&](int h) -> const E* {
+      if (h < p.Hq) return qs + (long long)h * kHeadDim;
+      h -= p.Hq;
+      return h < p.Hkv ? ks + (long long)h * kHeadDim : vs + (long long)(h - p.Hkv) * kHeadDim;
+    };
+    Vec8<E> a[kAppendItems], b[kAppendItems];
+    auto load = [&](int h0) {
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {
-      const int r = r0 + k * (kRopeThreads / kNs);
-      if (r < rows) {
-        const int t = r / heads, h = r - t * heads;
-        const E* src = source(t, h);
-        a[k].load(src + ca);
-        b[k].load(src + cb);
+      for (int k = 0; k < kAppendItems; ++k) {
+        const int h = h0 + 4 * k;
+        if (h < heads) {
+          const E* src = source(h);
+          a[k].load(src + ca);
+          b[k].load(src + cb);
+        }
       }
+    };
+    if (!SCALAR) load(g);               // in flight while the slot and the angles are worked out
+    const int sq = tok / p.T, i = tok - sq * p.T;
+    const int P = p.seq_lens ? __ldg(p.seq_lens + sq) : 0;
+    const int w = p.row_lens ? __ldg(p.row_lens + sq) : p.T;
+    const long long pos = (long long)(p.pos0 ? __ldg(p.pos0 + sq) : P) + i;
+    // Padding, or a sequence whose lengths are invalid: nothing is written.
+    if (P < 0 || w < 0 || w > p.T || (long long)P + w > p.S || i >= w) continue;
+    const int slot = P + i;
+    long long row, head_rows;           // cache row of KV head 0 (-1: none), rows between heads
+    if (p.block_table) {
+      const int page = __ldg(p.block_table + (size_t)sq * p.pages_per_seq + slot / p.page_size);
+      row = page >= 0 && page < p.num_pages ? (long long)page * p.Hkv * p.page_size + slot % p.page_size : -1;
+      head_rows = p.page_size;
+    } else {
+      row = (long long)sq * p.Hkv * p.S + slot;
+      head_rows = p.S;
     }
-    if (first) angles();
-    first = false;
+    if (p.key_pos && row >= 0)
+      for (int h = lane; h < p.Hkv; h += 32) p.key_pos[((size_t)sq * p.Hkv + h) * p.S + slot] = (int)pos;
+    auto target = [&](int h) -> E* {    // null: not written
+      if (h < p.Hq) return p.q_out + ((long long)tok * p.Hq + h) * kHeadDim;
+      if (row < 0) return nullptr;
+      h -= p.Hq;
+      return h < p.Hkv ? p.kc + (row + h * head_rows) * kHeadDim
+                       : p.vc + (row + (h - p.Hkv) * head_rows) * kHeadDim;
+    };
+    __syncwarp();                       // the previous token's table has been read
+    if (lane < pairs) table[SCALAR ? lane : table_at(lane, rot)] = turn_at(f0, pl.out_scale, pos);
+    if (lane + 32 < pairs) table[SCALAR ? lane + 32 : table_at(lane + 32, rot)] = turn_at(f1, pl.out_scale, pos);
+    __syncwarp();
+    if (SCALAR) {
+      for (int it = lane; it < heads * (kHeadDim / 2); it += 32) {
+        const int h = it / (kHeadDim / 2), j = it % (kHeadDim / 2);
+        E* dst = target(h);
+        if (!dst) continue;
+        const E* src = source(h);
+        const int xa = (HALF && j < pairs) ? j : 2 * j, xb = (HALF && j < pairs) ? j + pairs : 2 * j + 1;
+        const E ea = src[xa], eb = src[xb];
+        if (j < pairs && h < p.Hq + p.Hkv) {
+          const float2 c = table[j];
+          const float u = to_f32(ea), v = to_f32(eb);
+          dst[xa] = __float2bfloat16_rn(fmaf(u, c.x, -(v * c.y)));
+          dst[xb] = __float2bfloat16_rn(fmaf(v, c.x, u * c.y));
+        } else {
+          dst[xa] = ea;
+          dst[xb] = eb;
+        }
+      }
+      continue;
+    }
+    Turn8 turn;
+    if (turns) turn.load(table, s, rot);
+    for (int h0 = g;; ) {
 #pragma unroll
-    for (int k = 0; k < kItems; ++k) {
-      const int r = r0 + k * (kRopeThreads / kNs);
-      if (r < rows) {
-        const int t = r / heads, h = r - t * heads;
-        E* dst = target(s_at[t], h);
+      for (int k = 0; k < kAppendItems; ++k) {
+        const int h = h0 + 4 * k;
+        E* dst = h < heads ? target(h) : nullptr;
         if (dst) {
-          if (rot && h < p.Hq + p.Hkv) rotate_item<HALF>(a[k], b[k], s_cs + t * pairs, 8 * s, pairs);
+          if (turns && h < p.Hq + p.Hkv) rotate_item<HALF>(a[k], b[k], turn, 8 * s, pairs);
           a[k].store(dst + ca);
           b[k].store(dst + cb);
         }
       }
+      h0 += 4 * kAppendItems;
+      if (h0 >= heads) break;
+      load(h0);
     }
   }
 }
@@ -393,11 +390,11 @@ cudaError_t launch_rope_t(const la_rope_plan& pl, const RopeProblem& p, bool vec
   // (few tokens) no more than spreads them over two blocks per SM.
   const int per_tok = p.heads * (vec ? p.head_dim / 16 : p.head_dim / 2);
   long long tok = (long long)kRopeThreads * kItemsOf<E> / per_tok;
-  if (tok > 4096 / pairs) tok = 4096 / pairs;
+  if (tok > 4096 / (pairs + 7)) tok = 4096 / (pairs + 7);
   if (tok > p.tokens / 296) tok = p.tokens / 296;
   if (tok < 1) tok = 1;
   const dim3 grid((unsigned)((p.tokens + tok - 1) / tok));
-  const size_t smem = (size_t)tok * pairs * sizeof(float2);
+  const size_t smem = (size_t)tok * ((pairs + 7) / 8 * 8) * sizeof(float2);
   if (vec)
     return half ? launch_pdl(rope_kernel<E, true>, grid, dim3(kRopeThreads), smem, s, pl, p, (int)tok)
                 : launch_pdl(rope_kernel<E, false>, grid, dim3(kRopeThreads), smem, s, pl, p, (int)tok);
@@ -422,20 +419,16 @@ cudaError_t launch_rope(const la_rope_plan& pl, const RopeProblem& p, int dtype,
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_rope_append(const la_rope_plan& pl, const RopeAppendProblem& p, cudaStream_t s) {
-  const long long tokens = (long long)p.B * p.T;
-  // Tokens per block: one full set of loads for every thread (6 at 16 + 2 + 2 heads), and few tokens
-  // spread over two blocks per SM.
-  long long tok = kRopeThreads * kItemsOf<__nv_bfloat16> / ((p.Hq + 2LL * p.Hkv) * (kHeadDim / 16));
-  if (tok > kAppendTok) tok = kAppendTok;
-  if (tok > tokens / 296) tok = tokens / 296;
-  if (tok < 1) tok = 1;
-  const dim3 grid((unsigned)((tokens + tok - 1) / tok));
+cudaError_t launch_rope_append(const la_rope_plan& pl, const RopeAppendProblem& p, int sms, cudaStream_t s) {
+  // One warp per token while they fit on the GPU at once, else as many tokens in turn.
+  const int tokens = p.B * p.T;
+  const int full = 6 * sms, blocks = (tokens + kAppendWarps - 1) / kAppendWarps;
+  const dim3 grid((unsigned)(blocks < full ? blocks : full)), block(32 * kAppendWarps);
   const bool half = pl.layout == LA_ROPE_HALF;
   if (half && pl.rotary_dim % 16 != 0)
-    return launch_pdl(rope_append_kernel<true, true>, grid, dim3(kRopeThreads), 0, s, pl, p, (int)tok);
-  return half ? launch_pdl(rope_append_kernel<true, false>, grid, dim3(kRopeThreads), 0, s, pl, p, (int)tok)
-              : launch_pdl(rope_append_kernel<false, false>, grid, dim3(kRopeThreads), 0, s, pl, p, (int)tok);
+    return launch_pdl(rope_append_kernel<true, true>, grid, block, 0, s, pl, p);
+  return half ? launch_pdl(rope_append_kernel<true, false>, grid, block, 0, s, pl, p)
+              : launch_pdl(rope_append_kernel<false, false>, grid, block, 0, s, pl, p);
 }
 
 }  // namespace la

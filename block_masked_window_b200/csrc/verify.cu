@@ -35,6 +35,41 @@ __device__ __forceinline__ double to_f64(__nv_bfloat16 x) { return (double)__bfl
 __device__ __forceinline__ double to_f64(__half x) { return (double)__half2float(x); }
 __device__ __forceinline__ double positive(double x) { return x > 0.0 ? x : 0.0; }   // (NaN: 0)
 
+// Sum of f(j, x(j), y(j)) over j = j0, j0 + 32, ... < end: kVUnroll loads of each in flight, the
+// last ones one by one only where the range is ragged.
+template <typename X, typename Y, typename F>
+__device__ __forceinline__ double sum_range(int j0, int end, X x, Y y, F f) {
+  double even = 0.0, odd = 0.0;
+  int j = j0;
+  for (; j + 32 * (kVUnroll - 1) < end; j += 32 * kVUnroll) {
+    decltype(x(0)) a[kVUnroll];
+    decltype(y(0)) b[kVUnroll];
+#pragma unroll
+    for (int i = 0; i < kVUnroll; ++i) {
+      a[i] = x(j + 32 * i);
+      b[i] = y(j + 32 * i);
+    }
+#pragma unroll
+    for (int i = 0; i < kVUnroll; i += 2) {
+      even += f(j + 32 * i, a[i], b[i]);
+      odd += f(j + 32 * (i + 1), a[i + 1], b[i + 1]);
+    }
+  }
+  if (j < end) {
+    decltype(x(0)) a[kVUnroll];
+    decltype(y(0)) b[kVUnroll];
+#pragma unroll
+    for (int i = 0; i < kVUnroll; ++i) {   // (past the end: the last entry again, not counted)
+      a[i] = x(min(j + 32 * i, end - 1));
+      b[i] = y(min(j + 32 * i, end - 1));
+    }
+#pragma unroll
+    for (int i = 0; i < kVUnroll; ++i)
+      if (j + 32 * i < end) even += f(j + 32 * i, a[i], b[i]);
+  }
+  return even + odd;
+}
+
 template <typename E>
 __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyProblem a) {
   cg::cluster_group cluster = cg::this_cluster();
@@ -91,30 +126,21 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyProblem a) {
   const double v = (double)__ldg(a.sample_u + b);
   // First the residual, where a draft was rejected; then, if that is empty, p itself.
   bool rest = rejected;
-  auto entry = [&](long long j, E x, E less) {
+  auto entry = [&](int j, E x, E less) {
     const double d = to_f64(x);
     return positive(!rest ? d : qr ? d - to_f64(less) : j == skip ? 0.0 : d);
   };
   for (int attempt = 0;; ++attempt) {
-    const long long w0 = min((long long)(rank * kVWarps + warp) * per, (long long)a.V);
-    const long long w1 = min(w0 + per, (long long)a.V);
+    const int w0 = (int)min((long long)(rank * kVWarps + warp) * per, (long long)a.V);
+    const int w1 = min(w0 + per, a.V);
     double sum = 0.0;
-    for (long long j0 = w0 + lane; j0 < w1; j0 += 32 * kVUnroll) {
-      E x[kVUnroll], y[kVUnroll];
-#pragma unroll
-      for (int i = 0; i < kVUnroll; ++i)
-        if (j0 + 32 * i < w1) x[i] = pr[j0 + 32 * i];
-      if (rest && qr) {
-#pragma unroll
-        for (int i = 0; i < kVUnroll; ++i)
-          if (j0 + 32 * i < w1) y[i] = qr[j0 + 32 * i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < kVUnroll; ++i) y[i] = x[i];   // (not used)
-      }
-#pragma unroll
-      for (int i = 0; i < kVUnroll; ++i)
-        if (j0 + 32 * i < w1) sum += entry(j0 + 32 * i, x[i], y[i]);
+    if (rest && qr) {
+      sum = sum_range(w0 + lane, w1, [&](int j) { return pr[j]; }, [&](int j) { return qr[j]; },
+                      [&](int, E x, E y) { return positive(to_f64(x) - to_f64(y)); });
+    } else {
+      const int without = rest ? skip : -1;
+      sum = sum_range(w0 + lane, w1, [&](int j) { return pr[j]; }, [&](int) { return 0; },
+                      [&](int j, E x, int) { return j == without ? 0.0 : positive(to_f64(x)); });
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -186,7 +212,7 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyProblem a) {
       for (int i = 0; i < 4; ++i) {
         const long long j = c0 + (long long)tid * m + i;
         e[i] = 0.0;
-        if (i < m && j < w1) e[i] = entry(j, pr[j], rest && qr ? qr[j] : pr[j]);
+        if (i < m && j < w1) e[i] = entry((int)j, pr[j], rest && qr ? qr[j] : pr[j]);
         mine += e[i];
       }
       double incl = mine;
