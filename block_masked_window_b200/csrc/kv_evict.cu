@@ -3,20 +3,25 @@
 // Selection, per (sequence b, KV head h) with P_b keys and L = min(P_b, budget): the L keys of
 // the highest rank stay. Rank: protected keys first (position < sink or >= next_pos - recent), then
 // by weight (a NaN ranks as -inf), equal ranks by the lower slot. The weight becomes an unsigned
-// key of the same order, and the L-th largest key is found by three histogram passes over its
-// bits (11, 11, 10 from the top) instead of a sort. One cluster of up to 8 CTAs per (b, h): each CTA
+// number of the same order (its key), and the L-th largest is found by narrowing an interval of
+// keys instead of sorting: a histogram of 512 bins over the interval tells in which bin it lies; when
+// at most kCand keys are left, they are ranked against one another. The first interval is that of the
+// weights at hand, at most kOctaves powers of two below the largest, so that one histogram nearly
+// always suffices whatever the weights' scale. One cluster of up to 8 CTAs per (b, h): each CTA
 // holds a contiguous part of the keys in shared memory, and the CTAs read one another's
-// histograms through distributed shared memory. A last pass in slot order decides the ties,
-// copies what stays where it is and lists the evicted slots below L (holes) and the kept slots from
-// L on (movers).
+// histograms and candidates through distributed shared memory (which moves about 9 bytes a clock and
+// SM: 512 bins, not the 2048 that would leave fewer candidates, keep its share below the barriers').
+// A last pass in slot order lists the evicted slots below L (holes) and the kept slots from L on
+// (movers).
 //
 // Moving: there are as many movers as holes, and mover k goes to hole k. Every hole lies below L
 // and every mover at or above it, so no row that is read is ever written: the moves need no
 // order among them, and the cost is the rows that change place, not the rows kept. (Closing the
-// gaps in order would move almost the whole cache for a handful of evicted keys.)
+// gaps in order would move almost the whole cache for a handful of evicted keys.) The second kernel
+// also copies the weights and positions of what stays in place, where the outputs are separate.
 //
-// Bound: selection is latency (a few dependent passes over 4 bytes per key); moving is memory,
-// 512 bytes read and 512 written per moved key and head.
+// Bound: selection is latency (dependent passes over 4 bytes per key, two or three cluster barriers);
+// moving is memory, 512 bytes read and 512 written per moved key and head.
 #include <cooperative_groups.h>
 
 #include "pbd_common.cuh"
@@ -28,9 +33,11 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kSelThreads = 512;
-constexpr int kBins = 2048;                // of the widest pass
+constexpr int kBins = kSelThreads;         // one bin per thread
 constexpr int kSelKeys = 8;                // keys of a thread in a tile
 constexpr int kSelTile = kSelKeys * kSelThreads;
+constexpr int kCand = kSelThreads / 2;     // candidates ranked directly, two threads each
+constexpr uint32_t kOctaves = 20;          // span of the first histogram, in powers of two
 
 // Unsigned key of the same order as the weight; NaN as -inf, -0 as +0.
 __device__ __forceinline__ uint32_t rank_of(float w) {
@@ -62,29 +69,31 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* warp_tot, u
   return x + (wid ? before : 0u);
 }
 
-// Counts digit d of the lanes for which `in` holds. Where one digit prevails (equal weights, zeros)
-// its lanes are counted with one addition; the rest add for themselves.
-__device__ __forceinline__ void count_digit(uint32_t* hist, uint32_t d, bool in) {
-  const uint32_t live = __ballot_sync(0xffffffffu, in);
-  if (live == 0) return;
-  const int first = __ffs(live) - 1;
-  const uint32_t d0 = __shfl_sync(0xffffffffu, d, first);
-  const uint32_t same = __ballot_sync(0xffffffffu, in && d == d0);
-  if (in && d != d0) atomicAdd(hist + d, 1u);
-  if ((threadIdx.x & 31) == first) atomicAdd(hist + d0, (uint32_t)__popc(same));
-}
+// What a CTA shows the others of its cluster.
+struct SelShared {
+  uint32_t hist[2][kBins];                 // (a buffer for every other histogram)
+  unsigned long long cand[kCand];          // candidates: key in the high word, ~slot in the low
+  uint32_t lowest, highest, guarded;       // of the unprotected keys; protected keys
+  uint32_t n_cand;
+  int holes, movers;
+};
 
-__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictProblem p, int cap) {
+__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictProblem p, int cap) {
   cg::cluster_group cluster = cg::this_cluster();
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  __shared__ __align__(16) uint32_t hist[3][kBins];
+  __shared__ __align__(16) SelShared sh;
+  __shared__ __align__(16) unsigned long long s_all[kCand];   // the cluster's candidates
   __shared__ uint32_t warp_tot[32];
-  __shared__ uint32_t s_bin, s_above;      // digit of the wanted key, keys above that digit
-  __shared__ uint32_t s_keep[kSelThreads]; // which keys of a tile stay, a byte of bits per thread
+  __shared__ uint32_t s_bin, s_above, s_count, s_mine;   // wanted bin: keys above, in it, before this CTA's
+  __shared__ unsigned long long s_last;    // the last candidate that stays
   extern __shared__ __align__(16) uint32_t s_key[];   // [cap] this CTA's keys (when they fit)
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int bh = blockIdx.x / C, b = bh / p.Hkv;
-  for (int i = tid; i < 3 * kBins; i += kSelThreads) (&hist[0][0])[i] = 0;
+  sh.hist[0][tid] = 0;
+  if (tid == 0) {
+    sh.lowest = 0xFFFFFFFFu;
+    sh.highest = sh.guarded = sh.n_cand = 0;
+  }
   pdl_trigger();
   pdl_wait();
   const int P = __ldg(p.seq_lens + b);
@@ -94,276 +103,415 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(EvictProbl
   const long long next = p.next_pos ? (long long)__ldg(p.next_pos + b) : (long long)n;
   const float* w = p.weights + (size_t)bh * p.S;
   const int* pos = p.key_pos ? p.key_pos + (size_t)bh * p.S : nullptr;
-  float* w_out = p.weights_out + (size_t)bh * p.S;
-  int* pos_out = p.key_pos_out ? p.key_pos_out + (size_t)bh * p.S : nullptr;
-  int* kept = p.kept_slots ? p.kept_slots + (size_t)bh * p.budget : nullptr;
-  EvictList* list = p.lists + (size_t)bh * kMaxEvictCtas + rank;
   int* holes = p.slots + ((size_t)bh * C + rank) * 2 * p.part;
   int* movers = holes + p.part;
+  uint32_t* hole_bits = p.hole_bits + (size_t)bh * p.bit_words;
+  // A single CTA needs no barrier of the cluster.
+  auto sync_all = [&]() {
+    if (C == 1) __syncthreads();
+    else cluster.sync();
+  };
 
-  // Slots without a key say so.
-  if (kept)
-    for (int j = Lk + rank * kSelThreads + tid; j < p.budget; j += C * kSelThreads) kept[j] = -1;
   if (rank == 0 && tid == 0 && !valid) atomicOr(&p.hdr->err, kErrSeqOverflow);
 
   // This CTA's keys [j0, j1).
-  const int part = min(((n + C - 1) / C + 3) & ~3, p.part);
+  const int part = min(((n + C - 1) / C + 31) & ~31, p.part);   // (whole words of bits)
   const int j0 = min(rank * part, n), j1 = min(j0 + part, n);
   auto key_of = [&](int at, float weight) -> uint32_t {
     return at < p.sink || (long long)at >= next - p.recent ? 0xFFFFFFFFu : rank_of(weight);
   };
-  // Keys t0 + tid + i * kSelThreads, all loads in flight together (0 past the end).
-  auto load_tile = [&](int t0, uint32_t (&k)[kSelKeys]) {
-    float x[kSelKeys];
-    int at[kSelKeys];
+  // A warp's keys of a tile are consecutive, 32 to a row: lane l holds key l of each row, so that
+  // ballots give the rows' order. All loads in flight together; a part of one tile keeps them in
+  // registers.
+  const int first = warp * 32 * kSelKeys + lane;
+  float wv[kSelKeys];
+  int pv[kSelKeys];
+  auto load_tile = [&](int t0, int end) {
 #pragma unroll
     for (int i = 0; i < kSelKeys; ++i) {
-      const int j = t0 + tid + i * kSelThreads;
-      x[i] = j < j1 ? w[j] : 0.f;
-      at[i] = pos && j < j1 ? pos[j] : j;
+      const int j = t0 + first + 32 * i;
+      wv[i] = j < end ? w[j] : 0.f;
+      pv[i] = pos && j < end ? pos[j] : j;
     }
-#pragma unroll
-    for (int i = 0; i < kSelKeys; ++i) k[i] = key_of(at[i], x[i]);
   };
-
-  uint32_t thr = 0, need_eq = 0, eq_before = 0;
-  bool all_eq = true;                      // every key equal to the threshold stays
+  const bool one_tile = part <= kSelTile;
   const bool evicts = Lk < n;              // (uniform over the cluster)
   const bool held = part <= cap;
+  if (one_tile) load_tile(j0, j1);
+
+  // Keys above `thr` stay, and of the keys equal to it those up to slot `thr_slot`, or the first
+  // need_eq of the cluster in slot order where they are counted.
+  uint32_t thr = 0, need_eq = 0, eq_before = 0;
+  int thr_slot = 0x7fffffff;
+  bool count_eq = false;
   if (evicts) {
-    uint32_t want = (uint32_t)Lk;          // keys still wanted from the current prefix's keys
-    __syncthreads();
+    uint32_t low = 0xFFFFFFFFu, high = 0, guarded = 0;
+#pragma unroll 1
+    for (int t0 = j0; t0 < j1; t0 += kSelTile) {
+      if (!one_tile) load_tile(t0, j1);
 #pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const int bits = pass == 2 ? 10 : 11;
-      const uint32_t mask = (1u << bits) - 1;
-      for (int t0 = j0; t0 < j1; t0 += kSelTile) {
-        uint32_t k[kSelKeys];
-        if (pass > 0 && held) {
-#pragma unroll
-          for (int i = 0; i < kSelKeys; ++i) {
-            const int j = t0 + tid + i * kSelThreads;
-            k[i] = j < j1 ? s_key[j - j0] : 0u;
-          }
-        } else {
-          load_tile(t0, k);
-          if (held) {
-#pragma unroll
-            for (int i = 0; i < kSelKeys; ++i) {
-              const int j = t0 + tid + i * kSelThreads;
-              if (j < j1) s_key[j - j0] = k[i];
-            }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kSelKeys; ++i) {
-          bool in = t0 + tid + i * kSelThreads < j1;
-          if (pass > 0) in = in && (k[i] >> (shift + bits)) == (thr >> (shift + bits));
-          count_digit(hist[pass], (k[i] >> shift) & mask, in);
+      for (int i = 0; i < kSelKeys; ++i) {
+        const int j = t0 + first + 32 * i;
+        const uint32_t k = key_of(pv[i], wv[i]);
+        if (j < j1) {
+          if (held) s_key[j - j0] = k;
+          const bool safe = k == 0xFFFFFFFFu;
+          guarded += safe;
+          low = min(low, safe ? 0xFFFFFFFFu : k);
+          high = max(high, safe ? 0u : k);
         }
       }
-      cluster.sync();
-      // Sum over the cluster, then the digit at which the count from the top reaches `want`.
-      // Thread t holds the four bins from top - 4t down.
-      constexpr int kPer = kBins / kSelThreads;
-      static_assert(kPer == 4, "bins of a thread");
-      const int top = (int)mask - kPer * tid;
-      uint32_t c[kPer] = {0, 0, 0, 0};     // c[0]: the highest bin
-      if (top > 0) {
-        uint4 v[kMaxEvictCtas];            // (all loads in flight together)
+    }
+    __syncthreads();                       // s_key, and sh is initialised
+    // f(key, slot) for this CTA's keys.
+    auto for_keys = [&](auto f) {
+#pragma unroll 4
+      for (int j = j0 + tid; j < j1; j += kSelThreads)
+        f(held ? s_key[j - j0] : key_of(pos ? pos[j] : j, w[j]), j);
+    };
+    low = __reduce_min_sync(0xffffffffu, low);
+    high = __reduce_max_sync(0xffffffffu, high);
+    guarded = __reduce_add_sync(0xffffffffu, guarded);
+    if (lane == 0) {
+      atomicMin(&sh.lowest, low);
+      atomicMax(&sh.highest, high);
+      atomicAdd(&sh.guarded, guarded);
+    }
+    sync_all();
+    {
+      const SelShared* o = cluster.map_shared_rank(&sh, lane < C ? lane : 0);
+      low = __reduce_min_sync(0xffffffffu, o->lowest);
+      high = __reduce_max_sync(0xffffffffu, o->highest);
+      guarded = __reduce_add_sync(0xffffffffu, lane < C ? o->guarded : 0u);
+    }
+    uint32_t want = (uint32_t)Lk;          // keys still wanted from [low, high]
+    if (guarded >= want) {
+      low = high = 0xFFFFFFFFu;            // protected keys alone: the lowest slots
+    } else {
+      want -= guarded;
+    }
+    for (int round = 0;; ++round) {
+      // Bin 0: below `base`; bin i > 0: 2^shift keys from base + (i - 1) 2^shift on.
+      const uint32_t span = kOctaves << 23;
+      const uint32_t base = round == 0 && high - low > span ? high - span : low;
+      int shift = 0;
+      while (((high - base) >> shift) > kBins - 2) ++shift;
+      uint32_t* hist = sh.hist[round & 1];
+      for_keys([&](uint32_t k, int) {
+        if (k >= low && k <= high) atomicAdd(&hist[k < base ? 0u : 1u + ((k - base) >> shift)], 1u);
+      });
+      sync_all();
+      sh.hist[(round + 1) & 1][tid] = 0;   // (read last before this barrier)
+      // Thread t holds the t-th bin from the top, over the cluster.
+      const int bin = kBins - 1 - tid;
+      uint32_t v[kMaxEvictCtas], sum = 0, mine = 0;   // (all loads in flight together)
 #pragma unroll
-        for (int r = 0; r < kMaxEvictCtas; ++r)
-          v[r] = r < C ? *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&hist[pass][top - 3], r))
-                       : make_uint4(0u, 0u, 0u, 0u);
+      for (int r = 0; r < kMaxEvictCtas; ++r)
+        v[r] = r < C ? cluster.map_shared_rank(&sh, r)->hist[round & 1][bin] : 0u;
 #pragma unroll
-        for (int r = 0; r < kMaxEvictCtas; ++r) {
-          c[0] += v[r].w;
-          c[1] += v[r].z;
-          c[2] += v[r].y;
-          c[3] += v[r].x;
-        }
+      for (int r = 0; r < kMaxEvictCtas; ++r) {
+        if (r < rank) mine += v[r];
+        sum += v[r];
       }
       uint32_t total;
-      const uint32_t sum = c[0] + c[1] + c[2] + c[3];
       const uint32_t incl = block_scan(sum, warp_tot, &total);
-      uint32_t above = incl - sum;
-      if (above < want && want <= incl) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          if (above < want && want <= above + c[i]) {
-            s_bin = (uint32_t)(top - i);
-            s_above = above;
-          }
-          above += c[i];
-        }
+      if (incl - sum < want && want <= incl) {
+        s_bin = (uint32_t)bin;
+        s_above = incl - sum;
+        s_count = sum;
+        s_mine = mine;
       }
       __syncthreads();
-      thr |= s_bin << shift;
+      const uint32_t in_bin = s_count;
       want -= s_above;
-      if (pass == 2) {
-        const uint32_t d = thr & mask;
-        uint32_t all = 0;
-        uint32_t x[kMaxEvictCtas];
-#pragma unroll
-        for (int r = 0; r < kMaxEvictCtas; ++r) x[r] = r < C ? *cluster.map_shared_rank(&hist[2][d], r) : 0u;
+      if (s_bin == 0) {
+        high = base - 1;
+      } else {
+        low = base + ((s_bin - 1) << shift);
+        high = min(high, low + ((1u << shift) - 1));
+      }
+      if (low == high || in_bin == want) {
+        // One key value, of which the first `want` in slot order stay, or a bin that stays whole.
+        thr = low;
+        count_eq = in_bin != want;
+        need_eq = want;
+        eq_before = s_mine;
+        break;
+      }
+      if (in_bin <= kCand) {
+        // The wanted key is the candidate with want - 1 candidates before it.
+        for_keys([&](uint32_t k, int j) {
+          if (k >= low && k <= high)
+            sh.cand[atomicAdd(&sh.n_cand, 1u)] = (unsigned long long)k << 32 | (uint32_t)~j;
+        });
+        sync_all();
+        uint32_t at = 0;                   // where CTA r's candidates go
 #pragma unroll
         for (int r = 0; r < kMaxEvictCtas; ++r) {
-          if (r < rank) eq_before += x[r];
-          all += x[r];
-        }
-        need_eq = want;
-        all_eq = need_eq == all;
-      }
-    }
-  }
-  // In slot order: what stays, the holes and the movers of this CTA's part.
-  const bool copy_w = p.weights_out != p.weights;
-  const bool copy_pos = pos_out && p.key_pos_out != p.key_pos;
-  uint32_t n_holes = 0, n_movers = 0;
-  for (int t0 = j0; t0 < j1; t0 += kSelTile) {
-    const int j = t0 + kSelKeys * tid;     // this thread's run of keys
-    const int cnt = max(0, min(kSelKeys, j1 - j));
-    uint32_t keep = (1u << cnt) - 1;       // bit e: key j + e stays
-    if (evicts) {
-      uint32_t above = 0, eq = 0;
-#pragma unroll
-      for (int e = 0; e < kSelKeys; ++e) {
-        if (e < cnt) {
-          const uint32_t k = held ? s_key[j + e - j0] : key_of(pos ? pos[j + e] : j + e, w[j + e]);
-          above |= (uint32_t)(k > thr) << e;
-          eq |= (uint32_t)(k == thr) << e;
-        }
-      }
-      keep = above | eq;
-      if (!all_eq) {                       // the lowest slots among equals
-        uint32_t total;
-        const uint32_t at = eq_before + block_scan(__popc(eq), warp_tot, &total) - __popc(eq);
-        eq_before += total;
-        uint32_t left = need_eq > at ? need_eq - at : 0u;
-        keep = above;
-#pragma unroll
-        for (int e = 0; e < kSelKeys; ++e) {
-          if ((eq >> e & 1) && left > 0) {
-            keep |= 1u << e;
-            --left;
+          if (r < C) {
+            const SelShared* o = cluster.map_shared_rank(&sh, r);
+            const uint32_t have = o->n_cand;
+            if ((uint32_t)tid < have) s_all[at + tid] = o->cand[tid];
+            at += have;
           }
         }
+        __syncthreads();
+        const uint32_t c = tid >> 1;
+        const unsigned long long own = c < in_bin ? s_all[c] : 0ull;
+        uint32_t before = 0;
+        for (uint32_t i = tid & 1; i < in_bin; i += 2) before += s_all[i] > own;
+        before += __shfl_xor_sync(0xffffffffu, before, 1);
+        if (c < in_bin && before == want - 1) s_last = own;
+        __syncthreads();
+        thr = (uint32_t)(s_last >> 32);
+        thr_slot = (int)~(uint32_t)s_last;
+        break;
       }
-      const int low = max(0, min(kSelKeys, Lk - j));   // keys of the run below the new length
-      const uint32_t below = (1u << low) - 1;
-      uint32_t hole = ~keep & below & ((1u << cnt) - 1), mover = keep & ~below;
-      uint32_t total;                      // two counts of at most kSelTile in one word
-      const uint32_t both = __popc(hole) | __popc(mover) << 16;
-      const uint32_t at = block_scan(both, warp_tot, &total) - both;
-      int* hp = holes + n_holes + (at & 0xFFFFu);
-      int* mp = movers + n_movers + (at >> 16);
-      for (; hole; hole &= hole - 1) *hp++ = j + __ffs(hole) - 1;
-      for (; mover; mover &= mover - 1) *mp++ = j + __ffs(mover) - 1;
-      n_holes += total & 0xFFFFu;
-      n_movers += total >> 16;
     }
-    // What stays in place, consecutive threads on consecutive slots.
-    s_keep[tid] = keep;
+  }
+  // In slot order: the holes and the movers of this CTA's part.
+  const uint32_t before = (1u << lane) - 1;
+  // Sum of a warp's x over the warps before it, and over all of them.
+  auto warps_before = [&](uint32_t x, uint32_t* total) {
+    __syncthreads();                       // warp_tot has been read
+    if (lane == 0) warp_tot[warp] = x;
     __syncthreads();
-    float wv[kSelKeys];
-    int pv[kSelKeys];
-    uint32_t in_place = 0;
-#pragma unroll
-    for (int i = 0; i < kSelKeys; ++i) {   // (all loads in flight before the stores)
-      const int x = tid + i * kSelThreads, s = t0 + x;
-      if (s < min(j1, Lk) && (s_keep[x / kSelKeys] >> (x % kSelKeys) & 1)) {
-        in_place |= 1u << i;
-        if (copy_w) wv[i] = w[s];
-        pv[i] = copy_pos && pos ? pos[s] : s;
-      }
-    }
+    uint32_t t = lane < kSelThreads / 32 ? warp_tot[lane] : 0u;
+    *total = __reduce_add_sync(0xffffffffu, t);
+    return __reduce_add_sync(0xffffffffu, lane < warp ? t : 0u);
+  };
+  uint32_t n_holes = 0, n_movers = 0;
+#pragma unroll 1
+  for (int t0 = j0; t0 < j1 && evicts; t0 += kSelTile) {
+    uint32_t keep[kSelKeys], eq[kSelKeys]; // a bit for each key of a row
+    if (!held) load_tile(t0, j1);
+    uint32_t n_eq = 0;
 #pragma unroll
     for (int i = 0; i < kSelKeys; ++i) {
-      const int s = t0 + tid + i * kSelThreads;
-      if (in_place >> i & 1) {
-        if (copy_w) w_out[s] = wv[i];
-        if (copy_pos) pos_out[s] = pv[i];
-        if (kept) kept[s] = s;
+      const int j = t0 + first + 32 * i;
+      const uint32_t k = j >= j1 ? 0u : held ? s_key[j - j0] : key_of(pv[i], wv[i]);
+      // (A bin that stays whole: thr is its lowest key.)
+      const bool same = k == thr && j <= thr_slot;
+      keep[i] = __ballot_sync(0xffffffffu, j < j1 && (k > thr || (same && !count_eq)));
+      eq[i] = __ballot_sync(0xffffffffu, j < j1 && same);
+      n_eq += __popc(eq[i]);
+    }
+    if (count_eq) {                        // the lowest slots among equals
+      uint32_t total;
+      uint32_t at = eq_before + warps_before(n_eq, &total);
+      eq_before += total;
+#pragma unroll
+      for (int i = 0; i < kSelKeys; ++i) {
+        keep[i] |= __ballot_sync(0xffffffffu, (eq[i] >> lane & 1) && at + __popc(eq[i] & before) < need_eq);
+        at += __popc(eq[i]);
       }
     }
-    __syncthreads();
+    uint32_t both = 0, total;              // holes, and movers in the high half (at most kSelTile)
+#pragma unroll
+    for (int i = 0; i < kSelKeys; ++i) {
+      const int j = t0 + first + 32 * i;
+      const bool stays = keep[i] >> lane & 1;
+      const uint32_t hm = __ballot_sync(0xffffffffu, j < j1 && j < Lk && !stays);
+      const uint32_t mm = __ballot_sync(0xffffffffu, j >= Lk && stays);
+      if (lane == 0 && j < j1 && j < Lk) hole_bits[j >> 5] = hm;
+      eq[i] = hm;                          // (equals are settled)
+      keep[i] = mm;
+      both += __popc(hm) + (__popc(mm) << 16);
+    }
+    const uint32_t at = warps_before(both, &total);
+    int* hp = holes + n_holes + (at & 0xFFFFu);
+    int* mp = movers + n_movers + (at >> 16);
+#pragma unroll
+    for (int i = 0; i < kSelKeys; ++i) {
+      const int j = t0 + first + 32 * i;
+      if (eq[i] >> lane & 1) hp[__popc(eq[i] & before)] = j;
+      if (keep[i] >> lane & 1) mp[__popc(keep[i] & before)] = j;
+      hp += __popc(eq[i]);
+      mp += __popc(keep[i]);
+    }
+    n_holes += total & 0xFFFFu;
+    n_movers += total >> 16;
   }
   if (tid == 0) {
-    list->holes = (int)n_holes;
-    list->movers = (int)n_movers;
-    list->len = valid ? Lk : P;            // the sequence's new length
+    sh.holes = (int)n_holes;
+    sh.movers = (int)n_movers;
   }
-  cluster.sync();   // no CTA leaves while another may read its histograms
+  sync_all();
+  // The first CTA writes where each CTA's holes and movers end in the head's order.
+  if (rank == 0 && tid < 32) {
+    int h = 0, m = 0;
+    if (lane < C) {
+      const SelShared* o = cluster.map_shared_rank(&sh, lane);
+      h = o->holes;
+      m = o->movers;
+    }
+#pragma unroll
+    for (int o = 1; o < kMaxEvictCtas; o <<= 1) {
+      const int a = __shfl_up_sync(0xffffffffu, h, o), c = __shfl_up_sync(0xffffffffu, m, o);
+      if (lane >= o) {
+        h += a;
+        m += c;
+      }
+    }
+    EvictList* list = p.lists + bh;
+    if (lane < kMaxEvictCtas) {
+      list->holes[lane] = h;
+      list->movers[lane] = m;
+    }
+    const int moves = __shfl_sync(0xffffffffu, m, kMaxEvictCtas - 1);
+    if (lane == 0) {
+      p.moves[bh] = moves;
+      p.kept_lens[bh] = Lk;
+      if (bh == b * p.Hkv) p.lens[b] = valid ? Lk : P;   // the sequence's new length
+    }
+  }
+  if (C > 1) cluster.sync();   // no CTA leaves while another may read its shared memory
 }
 
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 4;               // keys a warp keeps in flight
-constexpr int kMoveCtas = 6;               // blocks per SM
+constexpr int kMoveCtas = 5;               // blocks per SM (48 registers a thread)
+constexpr int kCopySlots = 4 * kMoveThreads;
+constexpr int kMoveHeads = 1024;           // heads whose moves a block of blocks shares out
 
-// Slot k of a list that is spread over the parts of C CTAs.
-__device__ __forceinline__ int list_at(const int* slots, const int* ends, int C, int part, int which, int k) {
+// Slot k of a list that is spread over the parts of the CTAs.
+__device__ __forceinline__ int list_at(const int* slots, const int (&ends)[kMaxEvictCtas], int part, int which,
+                                       int k) {
   int r = 0, before = 0;
-  while (r + 1 < C && k >= ends[r]) {
-    before = ends[r];
-    ++r;
+#pragma unroll
+  for (int i = 0; i < kMaxEvictCtas - 1; ++i) {
+    if (k >= ends[i]) {
+      r = i + 1;
+      before = ends[i];
+    }
   }
   return slots[((size_t)r * 2 + which) * part + (k - before)];
 }
 
+// blockIdx.y: a group of kMoveHeads heads. Its moves are cut into pieces of kMoveRows, and the
+// warps of the group's blocks stride over all of them, so heads with many moves and heads with
+// none share the GPU evenly.
 __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) evict_move_kernel(EvictProblem p, int C) {
-  __shared__ int s_holes[kMaxEvictCtas], s_movers[kMaxEvictCtas];
-  const int bh = blockIdx.y, b = bh / p.Hkv, h = bh - b * p.Hkv;
+  __shared__ int s_end[kMoveHeads];        // pieces up to and including a head
+  __shared__ int s_warp[kMoveThreads / 32];
+  constexpr int kPer = kMoveHeads / kMoveThreads;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h0 = blockIdx.y * kMoveHeads, heads = min(kMoveHeads, p.B * p.Hkv - h0);
   pdl_trigger();
   pdl_wait();
-  const EvictList* list = p.lists + (size_t)bh * kMaxEvictCtas;
-  if (threadIdx.x == 0) {
-    int a = 0, m = 0;
-    for (int r = 0; r < C; ++r) {
-      s_holes[r] = a += list[r].holes;
-      s_movers[r] = m += list[r].movers;
-    }
-    if (blockIdx.x == 0 && h == 0) p.new_lens[b] = list[0].len;
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int b = tid; b < p.B; b += kMoveThreads) p.new_lens[b] = p.lens[b];
+  int cnt[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int h = tid * kPer + i;
+    cnt[i] = h < heads ? (p.moves[h0 + h] + kMoveRows - 1) / kMoveRows : 0;
+    sum += cnt[i];
   }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_warp[warp] = incl;
   __syncthreads();
-  const int moves = s_movers[C - 1];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int* slots = p.slots + (size_t)bh * C * 2 * p.part;
-  float* w_out = p.weights_out + (size_t)bh * p.S;
-  const float* w = p.weights + (size_t)bh * p.S;
+  int at = incl - sum, pieces = 0;
+#pragma unroll
+  for (int i = 0; i < kMoveThreads / 32; ++i) {
+    if (i < warp) at += s_warp[i];
+    pieces += s_warp[i];
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) s_end[tid * kPer + i] = at += cnt[i];
+  __syncthreads();
+
+  // What stays in place: the weight, position and origin of slots without a hole. Chunks of
+  // kCopySlots slots of a head, from the last block on (the moves start at the first).
+  const bool copy_w = p.weights_out != p.weights;
+  const bool copy_pos = p.key_pos_out && p.key_pos_out != p.key_pos;
+  if (copy_w || copy_pos || p.kept_slots) {
+    const int per_head = (p.budget + kCopySlots - 1) / kCopySlots;
+    for (long long c = gridDim.x - 1 - blockIdx.x; c < (long long)heads * per_head; c += gridDim.x) {
+      const int bh = h0 + (int)(c / per_head), s0 = (int)(c % per_head) * kCopySlots;
+      const int len = p.kept_lens[bh];       // slots that hold a key afterwards
+      const bool any = p.moves[bh] > 0;
+      const size_t row = (size_t)bh * p.S;
+      float x[kCopySlots / kMoveThreads];
+      int t[kCopySlots / kMoveThreads];
+      uint32_t stays = 0;
+#pragma unroll
+      for (int i = 0; i < kCopySlots / kMoveThreads; ++i) {
+        const int j = s0 + tid + i * kMoveThreads;
+        const uint32_t holes = any && j < len ? p.hole_bits[(size_t)bh * p.bit_words + (j >> 5)] : 0u;
+        if (j < len && copy_w) x[i] = p.weights[row + j];
+        t[i] = j < len && copy_pos && p.key_pos ? p.key_pos[row + j] : j;
+        stays |= (uint32_t)(j < len && !(holes >> (j & 31) & 1)) << i;
+      }
+#pragma unroll
+      for (int i = 0; i < kCopySlots / kMoveThreads; ++i) {
+        const int j = s0 + tid + i * kMoveThreads;
+        if (stays >> i & 1) {
+          if (copy_w) p.weights_out[row + j] = x[i];
+          if (copy_pos) p.key_pos_out[row + j] = t[i];
+          if (p.kept_slots) p.kept_slots[(size_t)bh * p.budget + j] = j;
+        } else if (p.kept_slots && j >= len && j < p.budget) {
+          p.kept_slots[(size_t)bh * p.budget + j] = -1;
+        }
+      }
+    }
+  }
+
   // Lanes 0..15 move a key's row of K, lanes 16..31 its row of V, 16 bytes each.
   uint4* cache = reinterpret_cast<uint4*>(lane < 16 ? p.kc : p.vc) + (lane & 15);
-  auto row = [&](int slot) -> long long {   // -1: the table names no page of the pool
+  auto row = [&](int bh, int slot) -> long long {   // -1: the table names no page of the pool
     if (!p.block_table) return ((long long)bh * p.S + slot) * (kHeadDim / 8);
+    const int b = bh / p.Hkv, h = bh - b * p.Hkv;
     const int page = __ldg(p.block_table + (size_t)b * p.pages_per_seq + slot / p.page_size);
     if (page < 0 || page >= p.num_pages) return -1;
     return (((long long)page * p.Hkv + h) * p.page_size + slot % p.page_size) * (kHeadDim / 8);
   };
-  const int stride = gridDim.x * (kMoveThreads / 32) * kMoveRows;
-  // Lane l < kMoveRows looks up move k0 + l (one turn ahead of the rows' copies).
-  auto look_up = [&](int k0, int& to, int& from) {
+  // Lane l < kMoveRows looks up move l of a piece (one turn ahead of the rows' copies).
+  auto look_up = [&](int piece, int& bh, int& to, int& from) {
     to = from = -1;
-    if (lane < kMoveRows && k0 + lane < moves) {
-      to = list_at(slots, s_holes, C, p.part, 0, k0 + lane);
-      from = list_at(slots, s_movers, C, p.part, 1, k0 + lane);
+    if (piece >= pieces) return;
+    int lo = 0, hi = heads - 1;            // the first head whose end lies beyond the piece
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s_end[mid] > piece) hi = mid;
+      else lo = mid + 1;
+    }
+    bh = h0 + lo;
+    const int k = (piece - (lo ? s_end[lo - 1] : 0)) * kMoveRows + lane;
+    const EvictList* list = p.lists + bh;
+    if (lane < kMoveRows && k < list->movers[kMaxEvictCtas - 1]) {
+      int ends[kMaxEvictCtas];
+      const int* slots = p.slots + (size_t)bh * C * 2 * p.part;
+#pragma unroll
+      for (int i = 0; i < kMaxEvictCtas; ++i) ends[i] = list->holes[i];
+      to = list_at(slots, ends, p.part, 0, k);
+#pragma unroll
+      for (int i = 0; i < kMaxEvictCtas; ++i) ends[i] = list->movers[i];
+      from = list_at(slots, ends, p.part, 1, k);
     }
   };
-  int k0 = (blockIdx.x * (kMoveThreads / 32) + warp) * kMoveRows;
-  int to, from, next_to, next_from;
-  look_up(k0, to, from);
-  for (; k0 < moves; k0 += stride) {
-    const long long rt = to >= 0 ? row(to) : -1, rf = from >= 0 ? row(from) : -1;
+  const int stride = gridDim.x * (kMoveThreads / 32);
+  int piece = blockIdx.x * (kMoveThreads / 32) + warp;
+  int bh = 0, to, from, next_bh = 0, next_to, next_from;
+  look_up(piece, bh, to, from);
+  for (; piece < pieces; piece += stride) {
+    const long long rt = to >= 0 ? row(bh, to) : -1, rf = from >= 0 ? row(bh, from) : -1;
     uint4 v[kMoveRows];
 #pragma unroll
     for (int i = 0; i < kMoveRows; ++i) {
       const long long f = __shfl_sync(0xffffffffu, rf, i);
       if (f >= 0) v[i] = __ldcs(cache + f);
     }
-    look_up(k0 + stride, next_to, next_from);
+    look_up(piece + stride, next_bh, next_to, next_from);
     if (to >= 0) {                          // the lane's own move: weight and position
-      w_out[to] = w[from];
-      if (p.key_pos_out)
-        p.key_pos_out[(size_t)bh * p.S + to] = p.key_pos ? p.key_pos[(size_t)bh * p.S + from] : from;
+      const size_t at = (size_t)bh * p.S;
+      p.weights_out[at + to] = p.weights[at + from];
+      if (p.key_pos_out) p.key_pos_out[at + to] = p.key_pos ? p.key_pos[at + from] : from;
       if (p.kept_slots) p.kept_slots[(size_t)bh * p.budget + to] = from;
     }
 #pragma unroll
@@ -371,6 +519,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) evict_move_kernel(Evi
       const long long f = __shfl_sync(0xffffffffu, rf, i), t = __shfl_sync(0xffffffffu, rt, i);
       if (f >= 0 && t >= 0) cache[t] = v[i];
     }
+    bh = next_bh;
     to = next_to;
     from = next_from;
   }
@@ -378,17 +527,23 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) evict_move_kernel(Evi
 
 }  // namespace
 
-int evict_ctas(int S) {
-  // One CTA per 4096 keys of capacity (eight keys a thread), at most a portable cluster.
-  int c = 1;
-  while (c < kMaxEvictCtas && c * kSelTile < S) c *= 2;
+int evict_ctas(int S, int heads) {
+  // One CTA up to 8192 keys of capacity (16 a thread), then one per 4096, at most a portable cluster,
+  // and no more than are resident together: a CTA takes an SM, and clusters of 8 leave up to a
+  // quarter of the SMs out (16 heads of 32768 keys: 8 CTAs each 28 us in two waves, 4 each 16 us).
+  if (S <= 2 * kSelTile) return 1;
+  int c = 2;
+  while (c < kMaxEvictCtas && c * kSelTile < S && 2 * c * heads <= 112) c *= 2;
   return c;
 }
 
-int evict_part(int S) { return ((S + evict_ctas(S) - 1) / evict_ctas(S) + 3) / 4 * 4; }
+int evict_part(int S, int heads) {
+  const int c = evict_ctas(S, heads);
+  return ((S + c - 1) / c + 31) / 32 * 32;
+}
 
 cudaError_t launch_evict(const EvictProblem& p, int sms, cudaStream_t s) {
-  const int C = evict_ctas(p.S);
+  const int C = evict_ctas(p.S, p.B * p.Hkv);
   constexpr int kMaxHeld = 40 * 1024;      // keys: 160 KB of shared memory
   const int cap = p.part <= kMaxHeld ? p.part : 0;
   const size_t smem = (size_t)cap * 4;
@@ -411,16 +566,17 @@ cudaError_t launch_evict(const EvictProblem& p, int sms, cudaStream_t s) {
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, cap);
   if (e != cudaSuccess) return e;
-  // Blocks per (sequence, KV head): enough for every possible move, but together no more than
-  // are resident at once (a block then takes several turns: one wave, evenly filled).
-  const int heads = p.B * p.Hkv;
+  // Blocks that are resident at once, in equal shares of the groups of heads; no more than for the
+  // most moves there can be and the chunks of what stays.
+  const int heads = p.B * p.Hkv, groups = (heads + kMoveHeads - 1) / kMoveHeads;
   const long long most = p.budget < p.S - p.budget ? p.budget : p.S - p.budget;
   const int per_block = kMoveThreads / 32 * kMoveRows;
-  long long x = (most + per_block - 1) / per_block;
-  const long long fill = (long long)kMoveCtas * sms / heads;
-  if (x > fill) x = fill;
+  const long long full = (most + per_block - 1) / per_block * (heads < kMoveHeads ? heads : kMoveHeads);
+  long long x = (long long)kMoveCtas * sms / groups;
+  const long long chunks = (long long)(p.budget + kCopySlots - 1) / kCopySlots * heads;
+  if (x > full + chunks) x = full + chunks;
   if (x < 1) x = 1;
-  return launch_pdl(evict_move_kernel, dim3((unsigned)x, (unsigned)heads), dim3(kMoveThreads), 0, s, p, C);
+  return launch_pdl(evict_move_kernel, dim3((unsigned)x, (unsigned)groups), dim3(kMoveThreads), 0, s, p, C);
 }
 
 }  // namespace la

@@ -189,16 +189,24 @@ la_status rope_append(const la_pbd_cfg* cfg, const la_rope_plan* plan, const voi
   return la::launch_rope_append(*plan, p, sms, (cudaStream_t)stream) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 
-// Workspace of la_kv_evict: header, list heads, lists.
+// Workspace of la_kv_evict: header, lists' ends, moves, lengths, hole bits, lists.
 struct EvictWs {
-  size_t lists, slots, total;
+  size_t lists, moves, kept_lens, lens, bits, slots, total;
+  int ctas, part, bit_words;
 };
 EvictWs evict_ws(const la_pbd_cfg* cfg, int S) {
   const size_t heads = (size_t)cfg->batch * cfg->num_kv_heads;
   EvictWs w;
+  w.ctas = la::evict_ctas(S, (int)heads);
+  w.part = la::evict_part(S, (int)heads);
+  w.bit_words = w.ctas * w.part / 32;
   w.lists = la::kHeaderBytes;
-  w.slots = w.lists + heads * la::kMaxEvictCtas * sizeof(la::EvictList);
-  w.total = w.slots + heads * la::evict_ctas(S) * 2 * (size_t)la::evict_part(S) * sizeof(int);
+  w.moves = w.lists + heads * sizeof(la::EvictList);
+  w.kept_lens = w.moves + heads * sizeof(int);
+  w.lens = w.kept_lens + heads * sizeof(int);
+  w.bits = w.lens + (size_t)cfg->batch * sizeof(int);
+  w.slots = w.bits + heads * w.bit_words * sizeof(uint32_t);
+  w.total = w.slots + heads * w.ctas * 2 * (size_t)w.part * sizeof(int);
   // Every workspace is at least what la_pbd_workspace_init takes.
   if (w.total < la::kSlotsOffset) w.total = la::kSlotsOffset;
   return w;
@@ -243,6 +251,11 @@ la_status kv_evict(const la_pbd_cfg* cfg, const float* weights, const int32_t* k
   p.new_lens = new_lens;
   p.hdr = reinterpret_cast<la::WsHeader*>(ws);
   p.lists = reinterpret_cast<la::EvictList*>(ws + w.lists);
+  p.moves = reinterpret_cast<int*>(ws + w.moves);
+  p.kept_lens = reinterpret_cast<int*>(ws + w.kept_lens);
+  p.lens = reinterpret_cast<int*>(ws + w.lens);
+  p.hole_bits = reinterpret_cast<uint32_t*>(ws + w.bits);
+  p.bit_words = w.bit_words;
   p.slots = reinterpret_cast<int*>(ws + w.slots);
   p.B = cfg->batch;
   p.Hkv = cfg->num_kv_heads;
@@ -250,7 +263,7 @@ la_status kv_evict(const la_pbd_cfg* cfg, const float* weights, const int32_t* k
   p.budget = budget;
   p.sink = sink;
   p.recent = recent;
-  p.part = la::evict_part(S);
+  p.part = w.part;
   return la::launch_evict(p, sms, (cudaStream_t)stream) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 

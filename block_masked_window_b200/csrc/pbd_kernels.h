@@ -95,8 +95,8 @@ cudaError_t launch_rope_append(const la_rope_plan& plan, const RopeAppendProblem
 
 // Eviction: see kv_evict.cu.
 constexpr int kMaxEvictCtas = 8;
-struct EvictList {
-  int holes, movers, len, pad;
+struct EvictList {              // of a (sequence, KV head): where each CTA's holes and movers end
+  int holes[kMaxEvictCtas], movers[kMaxEvictCtas];
 };
 struct EvictProblem {
   const float* weights;         // [B, Hkv, S]
@@ -107,13 +107,16 @@ struct EvictProblem {
   float* weights_out;
   int32_t *key_pos_out, *kept_slots, *new_lens;   // the first two may be null
   WsHeader* hdr;
-  EvictList* lists;             // [B * Hkv, kMaxEvictCtas]
+  EvictList* lists;             // [B * Hkv]
+  int *moves, *kept_lens, *lens;   // [B * Hkv] keys that change place, keys that stay; [B] new lengths
+  uint32_t* hole_bits;          // [B * Hkv, bit_words]: evicted slots, a bit each
+  int bit_words;                // of a head: slots of all CTAs' parts / 32
   int* slots;                   // [B * Hkv, CTAs, 2, part]: holes, movers
   int B, Hkv, S, budget, sink, recent;
   int part;                     // most keys of a CTA
 };
-int evict_ctas(int S);          // CTAs of a (sequence, KV head)
-int evict_part(int S);
+int evict_ctas(int S, int heads);   // CTAs of a (sequence, KV head)
+int evict_part(int S, int heads);
 cudaError_t launch_evict(const EvictProblem& p, int sms, cudaStream_t stream);
 
 // Verification of drafted tokens: see verify.cu. Strides in elements.
