@@ -37,7 +37,7 @@ constexpr int kBins = kSelThreads;         // one bin per thread
 constexpr int kSelKeys = 8;                // keys of a thread in a tile
 constexpr int kSelTile = kSelKeys * kSelThreads;
 constexpr int kCand = kSelThreads / 2;     // candidates ranked directly, two threads each
-constexpr uint32_t kOctaves = 20;          // span of the first histogram, in powers of two
+constexpr uint32_t kOctaves = 16;          // span of the first histogram, in powers of two
 
 // Unsigned key of the same order as the weight; NaN as -inf, -0 as +0.
 __device__ __forceinline__ uint32_t rank_of(float w) {
@@ -369,30 +369,35 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictProbl
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 4;               // keys a warp keeps in flight
-constexpr int kMoveCtas = 5;               // blocks per SM (48 registers a thread)
+constexpr int kMoveRows = 8;               // keys a warp keeps in flight
+constexpr int kMoveCtas = 4;               // blocks per SM
 constexpr int kCopySlots = 4 * kMoveThreads;
 constexpr int kMoveHeads = 1024;           // heads whose moves a block of blocks shares out
 
-// Slot k of a list that is spread over the parts of the CTAs.
-__device__ __forceinline__ int list_at(const int* slots, const int (&ends)[kMaxEvictCtas], int part, int which,
-                                       int k) {
+// Slot k of a list that is spread over the parts of C CTAs, which end at ends[0 .. C - 1].
+__device__ __forceinline__ int list_at(const int* slots, const int* ends, int C, int part, int which, int k) {
   int r = 0, before = 0;
+  if (C > 1) {
+    int e[kMaxEvictCtas - 1];
 #pragma unroll
-  for (int i = 0; i < kMaxEvictCtas - 1; ++i) {
-    if (k >= ends[i]) {
-      r = i + 1;
-      before = ends[i];
+    for (int i = 0; i < kMaxEvictCtas - 1; ++i) e[i] = ends[i];
+#pragma unroll
+    for (int i = 0; i < kMaxEvictCtas - 1; ++i) {
+      if (k >= e[i]) {
+        r = i + 1;
+        before = e[i];
+      }
     }
   }
   return slots[((size_t)r * 2 + which) * part + (k - before)];
 }
 
-// blockIdx.y: a group of kMoveHeads heads. Its moves are cut into pieces of kMoveRows, and the
-// warps of the group's blocks stride over all of them, so heads with many moves and heads with
-// none share the GPU evenly.
+// blockIdx.y: a group of kMoveHeads heads. Its moves are laid end to end and cut into one run for
+// each warp of the group's blocks, equal to +-1, so heads with many moves and heads with none share
+// the GPU evenly. The 32 lanes look up 32 moves of the run at once (head, slots, rows), and the warp
+// then copies their rows, kMoveRows at a time.
 __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) evict_move_kernel(EvictProblem p, int C) {
-  __shared__ int s_end[kMoveHeads];        // pieces up to and including a head
+  __shared__ int s_end[kMoveHeads];        // moves up to and including a head
   __shared__ int s_warp[kMoveThreads / 32];
   constexpr int kPer = kMoveHeads / kMoveThreads;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -405,7 +410,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) evict_move_kernel(Evi
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int h = tid * kPer + i;
-    cnt[i] = h < heads ? (p.moves[h0 + h] + kMoveRows - 1) / kMoveRows : 0;
+    cnt[i] = h < heads ? p.moves[h0 + h] : 0;
     sum += cnt[i];
   }
   int incl = sum;
@@ -416,11 +421,11 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) evict_move_kernel(Evi
   }
   if (lane == 31) s_warp[warp] = incl;
   __syncthreads();
-  int at = incl - sum, pieces = 0;
+  int at = incl - sum, total = 0;
 #pragma unroll
   for (int i = 0; i < kMoveThreads / 32; ++i) {
     if (i < warp) at += s_warp[i];
-    pieces += s_warp[i];
+    total += s_warp[i];
   }
 #pragma unroll
   for (int i = 0; i < kPer; ++i) s_end[tid * kPer + i] = at += cnt[i];
@@ -471,57 +476,44 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) evict_move_kernel(Evi
     if (page < 0 || page >= p.num_pages) return -1;
     return (((long long)page * p.Hkv + h) * p.page_size + slot % p.page_size) * (kHeadDim / 8);
   };
-  // Lane l < kMoveRows looks up move l of a piece (one turn ahead of the rows' copies).
-  auto look_up = [&](int piece, int& bh, int& to, int& from) {
-    to = from = -1;
-    if (piece >= pieces) return;
-    int lo = 0, hi = heads - 1;            // the first head whose end lies beyond the piece
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (s_end[mid] > piece) hi = mid;
-      else lo = mid + 1;
-    }
-    bh = h0 + lo;
-    const int k = (piece - (lo ? s_end[lo - 1] : 0)) * kMoveRows + lane;
-    const EvictList* list = p.lists + bh;
-    if (lane < kMoveRows && k < list->movers[kMaxEvictCtas - 1]) {
-      int ends[kMaxEvictCtas];
+  const int warps = gridDim.x * (kMoveThreads / 32), w = blockIdx.x * (kMoveThreads / 32) + warp;
+  const int end = (int)((w + 1LL) * total / warps);
+  for (int m0 = (int)((long long)w * total / warps); m0 < end; m0 += 32) {
+    const int cnt = min(32, end - m0);
+    long long rt = -1, rf = -1;
+    if (lane < cnt) {
+      const int m = m0 + lane;
+      int lo = 0, hi = heads - 1;          // the first head whose end lies beyond the move
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (s_end[mid] > m) hi = mid;
+        else lo = mid + 1;
+      }
+      const int bh = h0 + lo, k = m - (lo ? s_end[lo - 1] : 0);
+      const EvictList* list = p.lists + bh;
       const int* slots = p.slots + (size_t)bh * C * 2 * p.part;
-#pragma unroll
-      for (int i = 0; i < kMaxEvictCtas; ++i) ends[i] = list->holes[i];
-      to = list_at(slots, ends, p.part, 0, k);
-#pragma unroll
-      for (int i = 0; i < kMaxEvictCtas; ++i) ends[i] = list->movers[i];
-      from = list_at(slots, ends, p.part, 1, k);
-    }
-  };
-  const int stride = gridDim.x * (kMoveThreads / 32);
-  int piece = blockIdx.x * (kMoveThreads / 32) + warp;
-  int bh = 0, to, from, next_bh = 0, next_to, next_from;
-  look_up(piece, bh, to, from);
-  for (; piece < pieces; piece += stride) {
-    const long long rt = to >= 0 ? row(bh, to) : -1, rf = from >= 0 ? row(bh, from) : -1;
-    uint4 v[kMoveRows];
-#pragma unroll
-    for (int i = 0; i < kMoveRows; ++i) {
-      const long long f = __shfl_sync(0xffffffffu, rf, i);
-      if (f >= 0) v[i] = __ldcs(cache + f);
-    }
-    look_up(piece + stride, next_bh, next_to, next_from);
-    if (to >= 0) {                          // the lane's own move: weight and position
-      const size_t at = (size_t)bh * p.S;
+      const int to = list_at(slots, list->holes, C, p.part, 0, k);
+      const int from = list_at(slots, list->movers, C, p.part, 1, k);
+      rt = row(bh, to);
+      rf = row(bh, from);
+      const size_t at = (size_t)bh * p.S;  // the lane's own move: weight and position
       p.weights_out[at + to] = p.weights[at + from];
       if (p.key_pos_out) p.key_pos_out[at + to] = p.key_pos ? p.key_pos[at + from] : from;
       if (p.kept_slots) p.kept_slots[(size_t)bh * p.budget + to] = from;
     }
+    for (int i0 = 0; i0 < cnt; i0 += kMoveRows) {
+      uint4 v[kMoveRows];
 #pragma unroll
-    for (int i = 0; i < kMoveRows; ++i) {
-      const long long f = __shfl_sync(0xffffffffu, rf, i), t = __shfl_sync(0xffffffffu, rt, i);
-      if (f >= 0 && t >= 0) cache[t] = v[i];
+      for (int i = 0; i < kMoveRows; ++i) {
+        const long long f = __shfl_sync(0xffffffffu, rf, i0 + i);
+        if (f >= 0) v[i] = __ldcs(cache + f);
+      }
+#pragma unroll
+      for (int i = 0; i < kMoveRows; ++i) {
+        const long long f = __shfl_sync(0xffffffffu, rf, i0 + i), t = __shfl_sync(0xffffffffu, rt, i0 + i);
+        if (f >= 0 && t >= 0) cache[t] = v[i];
+      }
     }
-    bh = next_bh;
-    to = next_to;
-    from = next_from;
   }
 }
 

@@ -269,11 +269,11 @@ __global__ void __launch_bounds__(kRopeThreads)
 // q_out, k rotated into the cache slot P_b + i, v copied there, its position into key_pos.
 //
 // One warp per token (warps stride over the tokens): lane l holds channels of item l % 8 of heads
-// l / 8, l / 8 + 4, ..., so that the 8 pairs it turns are the same for all of them. The lanes
+// l / 8, l / 8 + 4, ... of q, and of k and v, so that the 8 pairs it turns are the same for all of them. The lanes
 // compute two pairs' cosines and sines each, exchange them through the warp's shared memory, and
 // keep their eight in registers. No barrier of the block, no division per item.
 constexpr int kAppendWarps = 4;         // per block
-constexpr int kAppendItems = 5;         // heads a lane keeps in flight (16 + 2 + 2 heads: all of them)
+constexpr int kAppendQ = 4;             // q heads a lane keeps in flight, besides one of k or v
 
 template <bool HALF, bool SCALAR>
 __global__ void __launch_bounds__(32 * kAppendWarps, 6)
@@ -292,27 +292,32 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 6)
   pdl_wait();
   const int tokens = p.B * p.T, step = gridDim.x * kAppendWarps;
   for (int tok = blockIdx.x * kAppendWarps + warp; tok < tokens; tok += step) {
-    const E* qs = p.q + (long long)tok * p.q_tok;
+    // The lane's first q head, and its first head of k and v: e < Hkv is k's, then v's.
+    const E* qs = p.q + (long long)tok * p.q_tok + (g * kHeadDim);
     const E* ks = p.k_new + (long long)tok * p.k_tok;
     const E* vs = p.v_new + (long long)tok * p.v_tok;
-    auto source = [&](int h) -> const E* {
-      if (h < p.Hq) return qs + (long long)h * kHeadDim;
-      h -= p.Hq;
-      return h < p.Hkv ? ks + (long long)h * kHeadDim : vs + (long long)(h - p.Hkv) * kHeadDim;
-    };
-    Vec8<E> a[kAppendItems], b[kAppendItems];
-    auto load = [&](int h0) {
+    auto kv_source = [&](int e) { return e < p.Hkv ? ks + e * kHeadDim : vs + (e - p.Hkv) * kHeadDim; };
+    Vec8<E> a[kAppendQ], b[kAppendQ], ka, kb;
+    auto load_q = [&](int h0) {
 #pragma unroll
-      for (int k = 0; k < kAppendItems; ++k) {
-        const int h = h0 + 4 * k;
-        if (h < heads) {
-          const E* src = source(h);
-          a[k].load(src + ca);
-          b[k].load(src + cb);
+      for (int k = 0; k < kAppendQ; ++k) {
+        if (h0 + g + 4 * k < p.Hq) {
+          a[k].load(qs + (h0 + 4 * k) * kHeadDim + ca);
+          b[k].load(qs + (h0 + 4 * k) * kHeadDim + cb);
         }
       }
     };
-    if (!SCALAR) load(g);               // in flight while the slot and the angles are worked out
+    auto load_kv = [&](int e) {
+      if (e < 2 * p.Hkv) {
+        const E* src = kv_source(e);
+        ka.load(src + ca);
+        kb.load(src + cb);
+      }
+    };
+    if (!SCALAR) {                      // in flight while the slot and the angles are worked out
+      load_q(0);
+      load_kv(g);
+    }
     const int sq = tok / p.T, i = tok - sq * p.T;
     const int P = p.seq_lens ? __ldg(p.seq_lens + sq) : 0;
     const int w = p.row_lens ? __ldg(p.row_lens + sq) : p.T;
@@ -331,12 +336,10 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 6)
     }
     if (p.key_pos && row >= 0)
       for (int h = lane; h < p.Hkv; h += 32) p.key_pos[((size_t)sq * p.Hkv + h) * p.S + slot] = (int)pos;
-    auto target = [&](int h) -> E* {    // null: not written
-      if (h < p.Hq) return p.q_out + ((long long)tok * p.Hq + h) * kHeadDim;
-      if (row < 0) return nullptr;
-      h -= p.Hq;
-      return h < p.Hkv ? p.kc + (row + h * head_rows) * kHeadDim
-                       : p.vc + (row + (h - p.Hkv) * head_rows) * kHeadDim;
+    E* qd = p.q_out + ((long long)tok * p.Hq + g) * kHeadDim;
+    auto kv_target = [&](int e) {
+      return (e < p.Hkv ? p.kc + (row + e * head_rows) * kHeadDim
+                        : p.vc + (row + (e - p.Hkv) * head_rows) * kHeadDim);
     };
     __syncwarp();                       // the previous token's table has been read
     if (lane < pairs) table[SCALAR ? lane : table_at(lane, rot)] = turn_at(f0, pl.out_scale, pos);
@@ -345,9 +348,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 6)
     if (SCALAR) {
       for (int it = lane; it < heads * (kHeadDim / 2); it += 32) {
         const int h = it / (kHeadDim / 2), j = it % (kHeadDim / 2);
-        E* dst = target(h);
-        if (!dst) continue;
-        const E* src = source(h);
+        if (h >= p.Hq && row < 0) continue;
+        E* dst = h < p.Hq ? p.q_out + ((long long)tok * p.Hq + h) * kHeadDim : kv_target(h - p.Hq);
+        const E* src = h < p.Hq ? p.q + (long long)tok * p.q_tok + h * kHeadDim : kv_source(h - p.Hq);
         const int xa = (HALF && j < pairs) ? j : 2 * j, xb = (HALF && j < pairs) ? j + pairs : 2 * j + 1;
         const E ea = src[xa], eb = src[xb];
         if (j < pairs && h < p.Hq + p.Hkv) {
@@ -364,20 +367,27 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 6)
     }
     Turn8 turn;
     if (turns) turn.load(table, s, rot);
-    for (int h0 = g;; ) {
+    for (int h0 = 0;;) {
 #pragma unroll
-      for (int k = 0; k < kAppendItems; ++k) {
-        const int h = h0 + 4 * k;
-        E* dst = h < heads ? target(h) : nullptr;
-        if (dst) {
-          if (turns && h < p.Hq + p.Hkv) rotate_item<HALF>(a[k], b[k], turn, 8 * s, pairs);
-          a[k].store(dst + ca);
-          b[k].store(dst + cb);
+      for (int k = 0; k < kAppendQ; ++k) {
+        if (h0 + g + 4 * k < p.Hq) {
+          if (turns) rotate_item<HALF>(a[k], b[k], turn, 8 * s, pairs);
+          a[k].store(qd + (h0 + 4 * k) * kHeadDim + ca);
+          b[k].store(qd + (h0 + 4 * k) * kHeadDim + cb);
         }
       }
-      h0 += 4 * kAppendItems;
-      if (h0 >= heads) break;
-      load(h0);
+      h0 += 4 * kAppendQ;
+      if (h0 >= p.Hq) break;
+      load_q(h0);
+    }
+    if (row < 0) continue;
+    for (int e = g; e < 2 * p.Hkv;) {
+      if (turns && e < p.Hkv) rotate_item<HALF>(ka, kb, turn, 8 * s, pairs);
+      E* dst = kv_target(e);
+      ka.store(dst + ca);
+      kb.store(dst + cb);
+      e += 4;
+      load_kv(e);
     }
   }
 }

@@ -29,6 +29,7 @@ constexpr int kVThreads = 512;
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kVMaxCtas = 8;
 constexpr int kVUnroll = 8;
+constexpr int kVRun = 5;         // entries of a thread when the draw's range is gone over again
 
 __device__ __forceinline__ double to_f64(float x) { return (double)x; }
 __device__ __forceinline__ double to_f64(__nv_bfloat16 x) { return (double)__bfloat162float(x); }
@@ -204,12 +205,12 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyProblem a) {
     // entry with any weight, where rounding lets none pass).
     const double goal = v * s_total;
     const long long w0 = (long long)range * per, w1 = min(w0 + per, (long long)a.V);
-    const int m = per > kVThreads ? 4 : 1;       // consecutive entries of a thread
+    const int m = min((per + kVThreads - 1) / kVThreads, kVRun);   // consecutive entries of a thread
     double run = s_before;
     for (long long c0 = w0; c0 < w1; c0 += (long long)kVThreads * m) {
-      double e[4], mine = 0.0;
+      double e[kVRun], mine = 0.0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kVRun; ++i) {
         const long long j = c0 + (long long)tid * m + i;
         e[i] = 0.0;
         if (i < m && j < w1) e[i] = entry((int)j, pr[j], rest && qr ? qr[j] : pr[j]);
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyProblem a) {
         run += s_scan[w];
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kVRun; ++i) {
         const long long j = c0 + (long long)tid * m + i;
         if (e[i] > 0.0) {
           atomicMax(&s_last, (int)j);
