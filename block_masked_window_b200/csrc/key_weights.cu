@@ -35,6 +35,7 @@ using namespace tc;
 constexpr int kWThreads = 192;
 constexpr int kWStages = 4;                 // K ring: 128 KB in flight per SM
 constexpr int kWSBufs = 4;                  // S^T buffers in TMEM
+constexpr int kAhead = 4;                   // tiles by which the old weights are read ahead
 constexpr int kWHalf = kTileKeys * 128;     // one 64-channel half of a K tile
 constexpr int kWTile = 2 * kWHalf;
 
@@ -125,44 +126,58 @@ __global__ void __launch_bounds__(kWThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      int g = 0, n = 0;
-      bool ok = true;
-      while (ok && it.next<true>(p, pre, blockIdx.x, sg)) {
-        const int qs = n & 1;
-        if (n > 1 && !mbar_wait(bar(kWBarQEmpty + qs), ((n >> 1) - 1) & 1, ctl)) break;
-        const uint32_t dq = sb + L.q + qs * 2 * kQHalf;
-        mbar_expect_tx(bar(kWBarQFull + qs), 2u * p.R * 128u);
-        tma_load_3d(dq, &tmq, bar(kWBarQFull + qs), 0, sg.h * p.G, sg.b * p.W);
-        tma_load_3d(dq + kQHalf, &tmq, bar(kWBarQFull + qs), 64, sg.h * p.G, sg.b * p.W);
-        ++n;
-        for (int jt = sg.j0; jt < sg.j1; jt += kTileKeys, ++g) {
+    // Lane 0 issues the copies. Of paged caches the whole warp looks up the pages of 16 tiles at once:
+    // a look-up per tile would hold each copy back by its latency.
+    int g = 0, n = 0;
+    bool ok = true;
+    while (ok && it.next<true>(p, pre, blockIdx.x, sg)) {
+      const int qs = n & 1;
+      if (lane == 0) {
+        if (n > 1 && !mbar_wait(bar(kWBarQEmpty + qs), ((n >> 1) - 1) & 1, ctl)) {
+          ok = false;
+        } else {
+          const uint32_t dq = sb + L.q + qs * 2 * kQHalf;
+          mbar_expect_tx(bar(kWBarQFull + qs), 2u * p.R * 128u);
+          tma_load_3d(dq, &tmq, bar(kWBarQFull + qs), 0, sg.h * p.G, sg.b * p.W);
+          tma_load_3d(dq + kQHalf, &tmq, bar(kWBarQFull + qs), 64, sg.h * p.G, sg.b * p.W);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      ++n;
+      int rows = 0;   // lane l: the pool row of the l-th half tile of 16 tiles
+      for (int jt = sg.j0; jt < sg.j1; jt += kTileKeys, ++g) {
+        const int t = (jt - sg.j0) / kTileKeys;
+        if (PAGED && (t & 15) == 0) {
+          // A half tile past the segment reads the segment's last page again (its rows are not
+          // used), so no table entry beyond the sequence is read.
+          const int j = min(jt + 64 * lane, sg.j1 - 1);
+          const int page = __ldcg(p.block_table + (size_t)sg.b * p.pages_per_seq + j / p.page_size);
+          rows = (page * p.Hkv + sg.h) * p.page_size + j % p.page_size;
+        }
+        const int row0 = PAGED ? __shfl_sync(0xffffffffu, rows, 2 * (t & 15)) : (sg.b * p.Hkv + sg.h) * p.S + jt;
+        const int row1 = PAGED ? __shfl_sync(0xffffffffu, rows, 2 * (t & 15) + 1) : 0;
+        if (lane == 0) {
           const int ks = g % kWStages;
           if (g >= kWStages && !mbar_wait(bar(kWBarKEmpty + ks), (g / kWStages - 1) & 1, ctl)) {
             ok = false;
-            break;
-          }
-          const uint32_t dk = sb + L.k + ks * kWTile, fb = bar(kWBarKFull + ks);
-          mbar_expect_tx(fb, (uint32_t)kWTile);
-          if (!PAGED) {
-            const int row = (sg.b * p.Hkv + sg.h) * p.S + jt;
-            tma_load_2d(dk, &tmk, fb, 0, row);
-            tma_load_2d(dk + kWHalf, &tmk, fb, 64, row);
           } else {
-            // 64-row boxes; a half tile past the segment reads the segment's last page again
-            // (its rows are not used), so no table entry beyond the sequence is read.
-#pragma unroll
-            for (int hr = 0; hr < 2; ++hr) {
-              int j = min(jt + 64 * hr, sg.j1 - 1);
-              const int page = __ldcg(p.block_table + (size_t)sg.b * p.pages_per_seq + j / p.page_size);
-              const int row = (page * p.Hkv + sg.h) * p.page_size + j % p.page_size;
-              tma_load_2d(dk + hr * 8192, &tmk, fb, 0, row);
-              tma_load_2d(dk + kWHalf + hr * 8192, &tmk, fb, 64, row);
+            const uint32_t dk = sb + L.k + ks * kWTile, fb = bar(kWBarKFull + ks);
+            mbar_expect_tx(fb, (uint32_t)kWTile);
+            tma_load_2d(dk, &tmk, fb, 0, row0);
+            tma_load_2d(dk + kWHalf, &tmk, fb, 64, row0);
+            if (PAGED) {   // (64-row boxes)
+              tma_load_2d(dk + 8192, &tmk, fb, 0, row1);
+              tma_load_2d(dk + kWHalf + 8192, &tmk, fb, 64, row1);
             }
           }
         }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
       }
-      // The copies issued last must have landed before shared memory is released.
+    }
+    // The copies issued last must have landed before shared memory is released.
+    if (lane == 0) {
       for (int back = 1; back <= kWStages && g - back >= 0; ++back)
         mbar_drain(bar(kWBarKFull + (g - back) % kWStages), ((g - back) / kWStages) & 1, 100000000LL);
       for (int back = 1; back <= 2 && n - back >= 0; ++back)
@@ -177,6 +192,15 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const int qs = n & 1;
         if (!mbar_wait(bar(kWBarQFull + qs), (n >> 1) & 1, ctl)) break;
         const uint32_t qb = sb + L.q + qs * 2 * kQHalf;
+        if (LIMITS && sg.w < p.W) {
+          // Padding rows of a shorter window may hold anything (a NaN): they become zeros, whose
+          // scores of 0 add 2^(0 - inf) = 0.
+          for (int i = sg.w * p.G * 8; i < p.R * 8; ++i) {
+            reinterpret_cast<uint4*>(base + L.q + qs * 2 * kQHalf)[i] = make_uint4(0u, 0u, 0u, 0u);
+            reinterpret_cast<uint4*>(base + L.q + qs * 2 * kQHalf + kQHalf)[i] = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_async_smem();
+        }
         for (int jt = sg.j0; jt < sg.j1; jt += kTileKeys, ++g) {
           const int ks = g % kWStages, s = g % kWSBufs;
           if (!mbar_wait(bar(kWBarKFull + ks), (g / kWStages) & 1, ctl) ||
@@ -223,12 +247,21 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (LIMITS) lim[q] = live ? row_limit(p, sg.n, sg.w, q) : 0;
       }
       __syncwarp();
+      // Window rows start afresh: their slots may hold the weight of an earlier occupant. The old
+      // weights are read kAhead tiles ahead (a tile takes less time than a read).
+      const int old_end = kw.in ? min(sg.n - sg.w, sg.j1) : 0;
+      auto old_at = [&](int key) { return key < old_end ? kw.in[head * p.S + key] : 0.f; };
+      float ahead[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) ahead[i] = old_at(sg.j0 + row + i * kTileKeys);
       for (int jt = sg.j0; jt < sg.j1; jt += kTileKeys, ++g) {
         const int key = jt + row, s = g % kWSBufs;
         const bool key_ok = key < sg.j1;
-        // Window rows start afresh: their slots may hold the weight of an earlier occupant.
-        float old = 0.f;
-        if (kw.in && key < sg.n - sg.w && key_ok) old = kw.decay * kw.in[head * p.S + key];
+        const bool edge = p.mask_mode != 0 && jt + kTileKeys > sg.n - sg.w;   // rows differ in what they see
+        const float old = ahead[0];
+#pragma unroll
+        for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
+        ahead[kAhead - 1] = old_at(key + kAhead * kTileKeys);
         ok = __all_sync(0xffffffffu, mbar_wait(bar(kWBarSFull + s), (g / kWSBufs) & 1, ctl));
         if (!ok) break;
         tc_fence_after();
@@ -251,12 +284,12 @@ __global__ void __launch_bounds__(kWThreads, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               float pr = fast_exp2(fmaf(x[e + i], c2, -l[i]));
-              if (LIMITS) pr = key < lim[c + e + i] ? pr : 0.f;
+              if (LIMITS && edge) pr = key < lim[c + e + i] ? pr : 0.f;
               sum[i] += pr;
             }
           }
         }
-        if (key_ok) kw.out[head * p.S + key] = old + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        if (key_ok) kw.out[head * p.S + key] = fmaf(kw.decay, old, (sum[0] + sum[1]) + (sum[2] + sum[3]));
       }
     }
   }

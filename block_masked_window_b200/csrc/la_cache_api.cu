@@ -128,7 +128,7 @@ la_status la_rope(const la_rope_plan* plan, int32_t dtype, const void* x, int64_
   p.y_head = out_head_stride;
   p.heads = heads;
   p.head_dim = head_dim;
-  p.sign = inverse ? -1.f : 1.f;
+  p.inverse = inverse != 0;
   return la::launch_rope(*plan, p, dtype, (cudaStream_t)stream) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 

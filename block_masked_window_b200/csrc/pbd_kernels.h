@@ -75,7 +75,7 @@ struct RopeProblem {
   const int32_t* positions;     // [tokens]
   long long tokens, x_tok, x_head, y_tok, y_head;
   int heads, head_dim;
-  float sign;                   // -1: inverse
+  bool inverse;
 };
 cudaError_t launch_rope(const la_rope_plan& plan, const RopeProblem& p, int dtype, cudaStream_t stream);
 

@@ -7,20 +7,25 @@
 // with (x1, x2) = channels (i, i + Rd/2) in the half layout and (2i, 2i + 1) in the
 // interleaved one; channels from Rd on are copied. The inverse turns by -a.
 //
-// Angles: t f_i is formed and reduced to a fraction of a turn in 64 bits (error below 2^-22
-// turns at t = 2^31), then sine and cosine are taken in 32 bits. A block computes the
+// Angles: f_i is handed to the kernels as a 64-bit fraction of a turn, so that t f_i modulo a turn is
+// one wrapping integer product (error below 2^-33 turns at t = 2^31; in 64-bit floating point the
+// product, its reduction and the conversions took a third of the kernel's instructions). Its upper
+// 32 bits become half turns in [-1, 1), of which sine and cosine are taken in 32 bits. A block computes the
 // cosines and sines of its tokens once into shared memory; every head of those tokens uses
 // them, so the transcendental work is 1/(heads) of the elements.
 //
 // Bound: memory. One item is 32 bytes of input (two 16-byte chunks, the two halves of 8 pairs in
 // the half layout) and 32 bytes of output, and a thread's loads are issued before the angles are
 // computed, so that the two overlap.
+#include <cmath>
+
 #include "pbd_common.cuh"
 #include "pbd_kernels.h"
 
 namespace la {
 namespace {
 
+constexpr int kMaxPairs = 128;
 constexpr int kRopeThreads = 256;
 // Items whose loads a thread keeps in flight: 128 bytes, with registers for four blocks an SM.
 template <typename E> constexpr int kItemsOf = sizeof(E) == 4 ? 2 : 4;
@@ -93,35 +98,66 @@ __device__ __forceinline__ void from_f32(float* d, float x) { *d = x; }
 __device__ __forceinline__ void from_f32(__nv_bfloat16* d, float x) { *d = __float2bfloat16_rn(x); }
 __device__ __forceinline__ void from_f32(__half* d, float x) { *d = __float2half_rn(x); }
 
-// (scaled cosine, scaled sine) at position t of a pair that makes f turns per position.
-__device__ __forceinline__ float2 turn_at(double f, float scale, long long t) {
-  const double turns = (double)t * f;
-  const float x = (float)(2.0 * (turns - rint(turns)));   // half turns in [-1, 1]
-  float s, c;
-  sincospif(x, &s, &c);
-  return make_float2(c * scale, s * scale);
-}
-__device__ __forceinline__ float2 turn_of(const la_rope_plan& pl, int i, long long t, float sign) {
-  float2 c = turn_at(pl.turns[i], pl.out_scale, t);
-  c.y *= sign;
-  return c;
+// A plan as the kernels take it.
+struct Turns {
+  int pairs;
+  float scale, sign;                       // sign: -1 turns back
+  unsigned long long f[kMaxPairs];         // fraction of a turn per position, times 2^64
+};
+Turns turns_of(const la_rope_plan& pl, bool inverse) {
+  Turns t;
+  t.pairs = pl.rotary_dim / 2;
+  t.scale = pl.out_scale;
+  t.sign = inverse ? -1.f : 1.f;
+  for (int i = 0; i < t.pairs; ++i) {
+    const double f = pl.turns[i] - std::floor(pl.turns[i]);          // (exact; a NaN stays one)
+    t.f[i] = f >= 0.0 && f < 1.0 ? (unsigned long long)(f * 18446744073709551616.0) : 0ull;
+  }
+  return t;
 }
 
-// Cosines and sines of a token are kept as two pairs to a float4, pairs 8s + 2e, 8s + 2e + 1 of
-// item s at [e][s]: neighbouring items (lanes) then read neighbouring 16-byte words.
-__device__ __forceinline__ int table_at(int pair, int rot) {   // rot = items that hold pairs
-  const int s = pair >> 3, e = (pair & 7) >> 1;
-  return 2 * (e * rot + s) + (pair & 1);                       // in float2
+// (scaled cosine, scaled sine) at position t of a pair that turns by the fraction f per position.
+__device__ __forceinline__ float2 turn_at(unsigned long long f, float scale, float sign, long long t) {
+  const int half = (int)((f * (unsigned long long)t) >> 32);         // of a turn, times 2^32
+  float s, c;
+  sincospif((float)half * 4.656612873077393e-10f, &s, &c);           // 2^-31: half turns
+  return make_float2(c * scale, s * scale * sign);
+}
+
+// Cosines and sines of a token are kept as a float4 (cos, cos, sin, sin) for two pairs, pairs 8s + 2e
+// and 8s + 2e + 1 of item s at [e][s]: neighbouring items (lanes) then read neighbouring 16-byte words,
+// and two pairs are turned by one packed instruction. rot = items that hold pairs.
+__device__ __forceinline__ void table_put(float* table, int pair, int rot, float2 cs) {
+  float* at = table + 4 * (((pair & 7) >> 1) * rot + (pair >> 3)) + (pair & 1);
+  at[0] = cs.x;
+  at[2] = cs.y;
 }
 struct Turn8 {
-  float4 cs[4];                                                // (cos, sin) of pairs 2e and 2e + 1
-  __device__ __forceinline__ void load(const float2* table, int s, int rot) {
+  float4 cs[4];
+  __device__ __forceinline__ void load(const float* table, int s, int rot) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) cs[e] = reinterpret_cast<const float4*>(table)[e * rot + s];
   }
-  __device__ __forceinline__ float cos_of(int e) const { return (e & 1) ? cs[e >> 1].z : cs[e >> 1].x; }
-  __device__ __forceinline__ float sin_of(int e) const { return (e & 1) ? cs[e >> 1].w : cs[e >> 1].y; }
+  __device__ __forceinline__ float cos_of(int e) const { return (e & 1) ? cs[e >> 1].y : cs[e >> 1].x; }
+  __device__ __forceinline__ float sin_of(int e) const { return (e & 1) ? cs[e >> 1].w : cs[e >> 1].z; }
 };
+
+// Two fp32 products, or products and sums, in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<unsigned long long&>(d))
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return d;
+}
 
 // Rotates the 16 channels of one item, pairs i0 .. i0 + 7. Half layout: a and b hold the pairs'
 // first and second channels. Interleaved: a holds pairs i0 .. i0 + 3 and b the next four;
@@ -133,10 +169,14 @@ __device__ __forceinline__ void rotate_item(Vec8<E>& a, Vec8<E>& b, const Turn8&
   b.get(y);
   if (HALF) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float c = t.cos_of(e), s = t.sin_of(e), u = x[e], w = y[e];
-      x[e] = fmaf(u, c, -(w * s));
-      y[e] = fmaf(w, c, u * s);
+    for (int e = 0; e < 4; ++e) {
+      const float2 c = make_float2(t.cs[e].x, t.cs[e].y), s = make_float2(t.cs[e].z, t.cs[e].w);
+      const float2 u = make_float2(x[2 * e], x[2 * e + 1]), w = make_float2(y[2 * e], y[2 * e + 1]);
+      const float2 p = fma2(u, c, mul2(w, make_float2(-s.x, -s.y))), q = fma2(w, c, mul2(u, s));
+      x[2 * e] = p.x;
+      x[2 * e + 1] = p.y;
+      y[2 * e] = q.x;
+      y[2 * e + 1] = q.y;
     }
   } else {
 #pragma unroll
@@ -176,12 +216,12 @@ __device__ __forceinline__ bool item_chunks(int s, int pairs, int* ca, int* cb) 
 // ---- Rotation alone: `tok` tokens per block.
 template <typename E, bool HALF>
 __global__ void __launch_bounds__(kRopeThreads, 4)
-    rope_kernel(const __grid_constant__ la_rope_plan pl, RopeProblem p, int tok) {
-  extern __shared__ __align__(16) float2 s_cs[];   // [tok][8 rot], see table_at
+    rope_kernel(const __grid_constant__ Turns pl, RopeProblem p, int tok) {
+  extern __shared__ __align__(16) float s_table[];   // [tok][16 rot], see table_put
   constexpr int kItems = kItemsOf<E>;
   pdl_trigger();
   pdl_wait();
-  const int pairs = pl.rotary_dim >> 1, rot = (pairs + 7) >> 3;
+  const int pairs = pl.pairs, rot = (pairs + 7) >> 3;
   const long long t0 = (long long)blockIdx.x * tok;
   const int nt = (int)min((long long)tok, p.tokens - t0);
   const int ns = p.head_dim >> 4;
@@ -206,7 +246,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
     if (base == threadIdx.x) {          // (first pass, every thread)
       for (int i = threadIdx.x; i < nt * pairs; i += kRopeThreads) {
         const int t = i / pairs, pair = i - t * pairs;
-        s_cs[t * 8 * rot + table_at(pair, rot)] = turn_of(pl, pair, __ldg(p.positions + t0 + t), p.sign);
+        table_put(s_table + t * 16 * rot, pair, rot,
+                  turn_at(pl.f[pair], pl.scale, pl.sign, __ldg(p.positions + t0 + t)));
       }
       __syncthreads();
     }
@@ -218,7 +259,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
         int ca, cb;
         if (item_chunks<HALF>(s, pairs, &ca, &cb)) {
           Turn8 turn;
-          turn.load(s_cs + t * 8 * rot, s, rot);
+          turn.load(s_table + t * 16 * rot, s, rot);
           rotate_item<HALF>(a[k], b[k], turn, 8 * s, pairs);
         }
         E* dst = y + (t0 + t) * p.y_tok + h * p.y_head;
@@ -232,16 +273,16 @@ __global__ void __launch_bounds__(kRopeThreads, 4)
 // The same for shapes and strides without 16-byte chunks: one thread per channel pair.
 template <typename E, bool HALF>
 __global__ void __launch_bounds__(kRopeThreads)
-    rope_scalar_kernel(const __grid_constant__ la_rope_plan pl, RopeProblem p, int tok) {
+    rope_scalar_kernel(const __grid_constant__ Turns pl, RopeProblem p, int tok) {
   extern __shared__ float2 s_cs[];
   pdl_trigger();
   pdl_wait();
-  const int pairs = pl.rotary_dim >> 1;
+  const int pairs = pl.pairs;
   const long long t0 = (long long)blockIdx.x * tok;
   const int nt = (int)min((long long)tok, p.tokens - t0);
   for (int i = threadIdx.x; i < nt * pairs; i += kRopeThreads) {
     const int t = i / pairs;
-    s_cs[i] = turn_of(pl, i - t * pairs, __ldg(p.positions + t0 + t), p.sign);
+    s_cs[i] = turn_at(pl.f[i - t * pairs], pl.scale, pl.sign, __ldg(p.positions + t0 + t));
   }
   __syncthreads();
   const int half = p.head_dim >> 1;
@@ -275,35 +316,47 @@ __global__ void __launch_bounds__(kRopeThreads)
 constexpr int kAppendWarps = 4;         // per block
 constexpr int kAppendQ = 4;             // q heads a lane keeps in flight, besides one of k or v
 
-template <bool HALF, bool SCALAR>
+// kWhole: the whole head turns. kPart: part of it. kScalar: no 16-byte chunks (half layout, rotary_dim
+// not a multiple of 16). The first is a form of its own because it needs no test per lane and pair.
+enum AppendForm { kWhole, kPart, kScalar };
+
+template <bool HALF, AppendForm FORM>
 __global__ void __launch_bounds__(32 * kAppendWarps, 6)
-    rope_append_kernel(const __grid_constant__ la_rope_plan pl, RopeAppendProblem p) {
+    rope_append_kernel(const __grid_constant__ Turns pl, RopeAppendProblem p) {
   using E = __nv_bfloat16;
-  __shared__ __align__(16) float2 s_cs[kAppendWarps][kHeadDim / 2];
+  __shared__ __align__(16) float s_table[kAppendWarps][kHeadDim];
+  constexpr bool SCALAR = FORM == kScalar;
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float2* table = s_cs[warp];
-  const int pairs = pl.rotary_dim >> 1, rot = (pairs + 7) >> 3;
-  const double f0 = lane < pairs ? pl.turns[lane] : 0.0, f1 = lane + 32 < pairs ? pl.turns[lane + 32] : 0.0;
+  float* table = s_table[warp];
+  const int pairs = FORM == kWhole ? kHeadDim / 2 : pl.pairs, rot = (pairs + 7) >> 3;
   const int heads = p.Hq + 2 * p.Hkv;
   const int s = lane & 7, g = lane >> 3;
+  // The lane's two pairs of the table: the float4 at [g][s] (see table_put).
+  const int own = 8 * s + 2 * g;
+  const unsigned long long f0 = own < pairs ? pl.f[own] : 0, f1 = own + 1 < pairs ? pl.f[own + 1] : 0;
   int ca, cb;
-  const bool turns = item_chunks<HALF>(s, pairs, &ca, &cb);
+  const bool turns = item_chunks<HALF>(s, pairs, &ca, &cb) || FORM == kWhole;
   pdl_wait();
   const int tokens = p.B * p.T, step = gridDim.x * kAppendWarps;
+  const bool whole_q = (p.Hq & 3) == 0;
   for (int tok = blockIdx.x * kAppendWarps + warp; tok < tokens; tok += step) {
-    // The lane's first q head, and its first head of k and v: e < Hkv is k's, then v's.
-    const E* qs = p.q + (long long)tok * p.q_tok + (g * kHeadDim);
+    // Heads g, g + 4, ... of q: where there are fewer, a lane repeats the last one (the same values to
+    // the same place), so that the loops are the warp's, not the lane's. Heads of k and v: e < Hkv is
+    // k's, then v's.
+    const E* qs = p.q + (long long)tok * p.q_tok;
     const E* ks = p.k_new + (long long)tok * p.k_tok;
     const E* vs = p.v_new + (long long)tok * p.v_tok;
     auto kv_source = [&](int e) { return e < p.Hkv ? ks + e * kHeadDim : vs + (e - p.Hkv) * kHeadDim; };
+    auto q_head = [&](int h) { return whole_q ? h + g : min(h + g, p.Hq - 1); };
     Vec8<E> a[kAppendQ], b[kAppendQ], ka, kb;
     auto load_q = [&](int h0) {
 #pragma unroll
       for (int k = 0; k < kAppendQ; ++k) {
-        if (h0 + g + 4 * k < p.Hq) {
-          a[k].load(qs + (h0 + 4 * k) * kHeadDim + ca);
-          b[k].load(qs + (h0 + 4 * k) * kHeadDim + cb);
+        if (h0 + 4 * k < p.Hq) {
+          const E* src = qs + q_head(h0 + 4 * k) * kHeadDim;
+          a[k].load(src + ca);
+          b[k].load(src + cb);
         }
       }
     };
@@ -336,14 +389,16 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 6)
     }
     if (p.key_pos && row >= 0)
       for (int h = lane; h < p.Hkv; h += 32) p.key_pos[((size_t)sq * p.Hkv + h) * p.S + slot] = (int)pos;
-    E* qd = p.q_out + ((long long)tok * p.Hq + g) * kHeadDim;
+    E* qd = p.q_out + (long long)tok * p.Hq * kHeadDim;
     auto kv_target = [&](int e) {
       return (e < p.Hkv ? p.kc + (row + e * head_rows) * kHeadDim
                         : p.vc + (row + (e - p.Hkv) * head_rows) * kHeadDim);
     };
     __syncwarp();                       // the previous token's table has been read
-    if (lane < pairs) table[SCALAR ? lane : table_at(lane, rot)] = turn_at(f0, pl.out_scale, pos);
-    if (lane + 32 < pairs) table[SCALAR ? lane + 32 : table_at(lane + 32, rot)] = turn_at(f1, pl.out_scale, pos);
+    if (own < pairs) {
+      const float2 c0 = turn_at(f0, pl.scale, pl.sign, pos), c1 = turn_at(f1, pl.scale, pl.sign, pos);
+      reinterpret_cast<float4*>(table)[g * rot + s] = make_float4(c0.x, c1.x, c0.y, c1.y);
+    }
     __syncwarp();
     if (SCALAR) {
       for (int it = lane; it < heads * (kHeadDim / 2); it += 32) {
@@ -354,7 +409,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 6)
         const int xa = (HALF && j < pairs) ? j : 2 * j, xb = (HALF && j < pairs) ? j + pairs : 2 * j + 1;
         const E ea = src[xa], eb = src[xb];
         if (j < pairs && h < p.Hq + p.Hkv) {
-          const float2 c = table[j];
+          const float* at = table + 4 * (((j & 7) >> 1) * rot + (j >> 3)) + (j & 1);
+          const float2 c = make_float2(at[0], at[2]);
           const float u = to_f32(ea), v = to_f32(eb);
           dst[xa] = __float2bfloat16_rn(fmaf(u, c.x, -(v * c.y)));
           dst[xb] = __float2bfloat16_rn(fmaf(v, c.x, u * c.y));
@@ -370,10 +426,11 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 6)
     for (int h0 = 0;;) {
 #pragma unroll
       for (int k = 0; k < kAppendQ; ++k) {
-        if (h0 + g + 4 * k < p.Hq) {
+        if (h0 + 4 * k < p.Hq) {
           if (turns) rotate_item<HALF>(a[k], b[k], turn, 8 * s, pairs);
-          a[k].store(qd + (h0 + 4 * k) * kHeadDim + ca);
-          b[k].store(qd + (h0 + 4 * k) * kHeadDim + cb);
+          E* dst = qd + q_head(h0 + 4 * k) * kHeadDim;
+          a[k].store(dst + ca);
+          b[k].store(dst + cb);
         }
       }
       h0 += 4 * kAppendQ;
@@ -393,9 +450,10 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 6)
 }
 
 template <typename E>
-cudaError_t launch_rope_t(const la_rope_plan& pl, const RopeProblem& p, bool vec, cudaStream_t s) {
-  const bool half = pl.layout == LA_ROPE_HALF;
-  const int pairs = pl.rotary_dim / 2;
+cudaError_t launch_rope_t(const la_rope_plan& plan, const RopeProblem& p, bool vec, cudaStream_t s) {
+  const Turns pl = turns_of(plan, p.inverse);
+  const bool half = plan.layout == LA_ROPE_HALF;
+  const int pairs = pl.pairs;
   // Tokens per block: a full set of loads for every thread, at most 32 KB of cosines and sines, and
   // (few tokens) no more than spreads them over two blocks per SM.
   const int per_tok = p.heads * (vec ? p.head_dim / 16 : p.head_dim / 2);
@@ -429,16 +487,18 @@ cudaError_t launch_rope(const la_rope_plan& pl, const RopeProblem& p, int dtype,
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_rope_append(const la_rope_plan& pl, const RopeAppendProblem& p, int sms, cudaStream_t s) {
+cudaError_t launch_rope_append(const la_rope_plan& plan, const RopeAppendProblem& p, int sms, cudaStream_t s) {
   // One warp per token while they fit on the GPU at once, else as many tokens in turn.
   const int tokens = p.B * p.T;
   const int full = 6 * sms, blocks = (tokens + kAppendWarps - 1) / kAppendWarps;
   const dim3 grid((unsigned)(blocks < full ? blocks : full)), block(32 * kAppendWarps);
-  const bool half = pl.layout == LA_ROPE_HALF;
-  if (half && pl.rotary_dim % 16 != 0)
-    return launch_pdl(rope_append_kernel<true, true>, grid, block, 0, s, pl, p);
-  return half ? launch_pdl(rope_append_kernel<true, false>, grid, block, 0, s, pl, p)
-              : launch_pdl(rope_append_kernel<false, false>, grid, block, 0, s, pl, p);
+  const Turns pl = turns_of(plan, false);
+  const bool half = plan.layout == LA_ROPE_HALF;
+#define LA_APPEND(HALF, FORM) launch_pdl(rope_append_kernel<HALF, FORM>, grid, block, 0, s, pl, p)
+  if (plan.rotary_dim == kHeadDim) return half ? LA_APPEND(true, kWhole) : LA_APPEND(false, kWhole);
+  if (half && plan.rotary_dim % 16 != 0) return LA_APPEND(true, kScalar);
+  return half ? LA_APPEND(true, kPart) : LA_APPEND(false, kPart);
+#undef LA_APPEND
 }
 
 }  // namespace la
