@@ -748,6 +748,28 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           tc_wait_ld();
           const float4* mr4 = reinterpret_cast<const float4*>(rowst + cur * NQ);
           bool exceeds = false;
+          if (CAUSAL) {
+            // Rows with limits of their own: only a tile that reaches past the prefix or the segment
+            // needs the masks; before it every row of the window sees every key (padding rows
+            // carry the reference +inf, so that their p is 0).
+#pragma unroll
+            for (int c4 = 0; c4 < NQ / 4; ++c4) {
+              const float4 m4 = mr4[c4];
+              x[4 * c4] = fmaf(x[4 * c4], c2, -m4.x);
+              x[4 * c4 + 1] = fmaf(x[4 * c4 + 1], c2, -m4.y);
+              x[4 * c4 + 2] = fmaf(x[4 * c4 + 2], c2, -m4.z);
+              x[4 * c4 + 3] = fmaf(x[4 * c4 + 3], c2, -m4.w);
+            }
+            if (jt + kNT > min(sg.n - sg.w, sg.j1)) {
+#pragma unroll
+              for (int q = 0; q < NQ; ++q) x[q] = key < lim_q[q] ? x[q] : -INFINITY;
+            }
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+              exceeds |= x[q] > kLazyThreshold;
+              x[q] = fast_exp2(x[q]);
+            }
+          } else {
 #pragma unroll
           for (int c4 = 0; c4 < NQ / 4; ++c4) {
             const float4 m4 = mr4[c4];
@@ -756,10 +778,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             for (int e = 0; e < 4; ++e) {
               const int q = 4 * c4 + e;
               const float y = fmaf(x[q], c2, -mq[e]);
-              const bool v = CAUSAL ? (key < lim_q[q]) : key_ok;
-              exceeds |= v && (y > kLazyThreshold);
-              x[q] = v ? fast_exp2(y) : 0.f;
+              exceeds |= key_ok && (y > kLazyThreshold);
+              x[q] = key_ok ? fast_exp2(y) : 0.f;
             }
+          }
           }
           // CTA-wide vote: raise the references only if some score is far above them.
           rescale = softmax_bar_or(exceeds);
@@ -804,9 +826,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             const int q = stid;
             const float tm = fmaxf(fmaxf(wm[q], wm[NQ + q]), fmaxf(wm[2 * NQ + q], wm[3 * NQ + q]));
             const float mo = rowst[cur * NQ + q];
-            const float mn = fmaxf(mo, tm);
+            const float mn = (CAUSAL && q >= sg.w * p.G) ? INFINITY : fmaxf(mo, tm);
             mw[q] = mn;
-            alpha_s[q] = (mn == -INFINITY) ? 1.f : fast_exp2(mo - mn);
+            alpha_s[q] = fabsf(mn) == INFINITY ? 1.f : fast_exp2(mo - mn);
           }
           // The previous PV product (and so every earlier one) must be complete before O and l
           // are rescaled in place (and before a single P^T buffer is rewritten).

@@ -17,8 +17,10 @@
 // Plan: as the attention kernel's, without a fixed segment cost: every CTA gets the same
 // number of whole key tiles, +-1, whatever the mix of lengths.
 //
-// Roles (192 threads, 1 CTA per SM): warp 0 TMA producer (Q per segment, double-buffered; K ring),
-// warp 1 TMEM owner and MMA issuer, warps 2..5 sums. Everything up to the first product only
+// Roles (320 threads, 1 CTA per SM): warp 0 TMA producer (Q per segment, double-buffered; K ring),
+// warp 1 TMEM owner and MMA issuer, warps 2..5 and 6..9 sums of every other tile (one warp per
+// scheduler took 1150 cycles for the 48 rows of a tile, more than its copy; two hide each other's
+// latencies). Everything up to the first product only
 // reads what was complete before the attention kernel started (the merge kernel starts after
 // every attention CTA's wait), so it runs while the merge is still working; the sums wait for it.
 // Every wait is bounded, as in the attention kernel.
@@ -32,16 +34,16 @@ namespace {
 
 using namespace tc;
 
-constexpr int kWThreads = 192;
-constexpr int kWStages = 4;                 // K ring: 128 KB in flight per SM
+constexpr int kWThreads = 320;               // 2 + 8 warps
+constexpr int kWMaxStages = 4;              // K ring: 128 KB in flight per SM (6 measured slower)
 constexpr int kWSBufs = 4;                  // S^T buffers in TMEM
 constexpr int kAhead = 4;                   // tiles by which the old weights are read ahead
 constexpr int kWHalf = kTileKeys * 128;     // one 64-channel half of a K tile
 constexpr int kWTile = 2 * kWHalf;
 
 constexpr int kWBarKFull = 0;
-constexpr int kWBarKEmpty = kWBarKFull + kWStages;
-constexpr int kWBarQFull = kWBarKEmpty + kWStages;   // [2]
+constexpr int kWBarKEmpty = kWBarKFull + kWMaxStages;
+constexpr int kWBarQFull = kWBarKEmpty + kWMaxStages;   // [2]
 constexpr int kWBarQEmpty = kWBarQFull + 2;          // [2]
 constexpr int kWBarSFull = kWBarQEmpty + 2;
 constexpr int kWBarSEmpty = kWBarSFull + kWSBufs;
@@ -49,17 +51,18 @@ constexpr int kWBarDrain = kWBarSEmpty + kWSBufs;
 constexpr int kWNumBars = kWBarDrain + 1;
 
 struct WLayout {
-  int k, q, bar, misc, lse, lim, pre, end;
+  int k, q, bar, misc, lse, lim, old, pre, end;
 };
-__host__ __device__ inline WLayout w_layout(int nq, int B) {
+__host__ __device__ inline WLayout w_layout(int nq, int stages, int B) {
   WLayout L;
   L.k = 0;
-  L.q = kWStages * kWTile;
+  L.q = stages * kWTile;
   L.bar = L.q + 2 * nq * 256;
   L.misc = L.bar + (kWNumBars + 1) / 2 * 16;
-  L.lse = L.misc + 16;                      // [4 warps][nq] floats (16-byte multiples)
-  L.lim = L.lse + 4 * nq * 4;               // [4][nq] ints
-  L.pre = L.lim + 4 * nq * 4;               // [B + 1] prefix sums, 32 ints
+  L.lse = L.misc + 16;                      // [8 warps][nq] floats (16-byte multiples)
+  L.lim = L.lse + 8 * nq * 4;               // [8][nq] ints
+  L.old = L.lim + 8 * nq * 4;               // [2 groups][kAhead][128] floats
+  L.pre = L.old + 2 * kAhead * 512;             // [B + 1] prefix sums, 32 ints
   L.end = L.pre + (round_up(B + 1, 4) + 32) * 4;
   return L;
 }
@@ -71,7 +74,7 @@ __host__ __device__ constexpr int w_tmem_cols(int nq) {
 template <int NQ, bool LIMITS, bool PAGED>
 __global__ void __launch_bounds__(kWThreads, 1)
     key_weights_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmq,
-                       Problem p, KeyWeights kw) {
+                       Problem p, KeyWeights kw, int stages) {
   constexpr int kQHalf = NQ * 128;
   constexpr int kCols = w_tmem_cols(NQ);
   static_assert(kWSBufs * NQ <= kCols, "TMEM columns");
@@ -79,7 +82,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
 
   extern __shared__ __align__(1024) char smem_raw[];
   char* base = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const WLayout L = w_layout(NQ, p.B);
+  const WLayout L = w_layout(NQ, stages, p.B);
   const uint32_t sb = smem_u32(base);
   auto bar = [&](int i) { return sb + (uint32_t)L.bar + 8u * (uint32_t)i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(base + L.misc);
@@ -128,6 +131,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
     // ------------------------------------------------------------------ TMA producer
     // Lane 0 issues the copies. Of paged caches the whole warp looks up the pages of 16 tiles at once:
     // a look-up per tile would hold each copy back by its latency.
+    const uint64_t policy = l2_policy_evict_first();   // read for the last time
     int g = 0, n = 0;
     bool ok = true;
     while (ok && it.next<true>(p, pre, blockIdx.x, sg)) {
@@ -158,17 +162,17 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const int row0 = PAGED ? __shfl_sync(0xffffffffu, rows, 2 * (t & 15)) : (sg.b * p.Hkv + sg.h) * p.S + jt;
         const int row1 = PAGED ? __shfl_sync(0xffffffffu, rows, 2 * (t & 15) + 1) : 0;
         if (lane == 0) {
-          const int ks = g % kWStages;
-          if (g >= kWStages && !mbar_wait(bar(kWBarKEmpty + ks), (g / kWStages - 1) & 1, ctl)) {
+          const int ks = g % stages;
+          if (g >= stages && !mbar_wait(bar(kWBarKEmpty + ks), (g / stages - 1) & 1, ctl)) {
             ok = false;
           } else {
             const uint32_t dk = sb + L.k + ks * kWTile, fb = bar(kWBarKFull + ks);
             mbar_expect_tx(fb, (uint32_t)kWTile);
-            tma_load_2d(dk, &tmk, fb, 0, row0);
-            tma_load_2d(dk + kWHalf, &tmk, fb, 64, row0);
+            tma_load_2d_hint(dk, &tmk, fb, 0, row0, policy);
+            tma_load_2d_hint(dk + kWHalf, &tmk, fb, 64, row0, policy);
             if (PAGED) {   // (64-row boxes)
-              tma_load_2d(dk + 8192, &tmk, fb, 0, row1);
-              tma_load_2d(dk + kWHalf + 8192, &tmk, fb, 64, row1);
+              tma_load_2d_hint(dk + 8192, &tmk, fb, 0, row1, policy);
+              tma_load_2d_hint(dk + kWHalf + 8192, &tmk, fb, 64, row1, policy);
             }
           }
         }
@@ -178,32 +182,34 @@ __global__ void __launch_bounds__(kWThreads, 1)
     }
     // The copies issued last must have landed before shared memory is released.
     if (lane == 0) {
-      for (int back = 1; back <= kWStages && g - back >= 0; ++back)
-        mbar_drain(bar(kWBarKFull + (g - back) % kWStages), ((g - back) / kWStages) & 1, 100000000LL);
+      for (int back = 1; back <= stages && g - back >= 0; ++back)
+        mbar_drain(bar(kWBarKFull + (g - back) % stages), ((g - back) / stages) & 1, 100000000LL);
       for (int back = 1; back <= 2 && n - back >= 0; ++back)
         mbar_drain(bar(kWBarQFull + ((n - back) & 1)), ((n - back) >> 1) & 1, 100000000LL);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      int g = 0, n = 0;
-      bool ok = true;
-      while (ok && it.next<true>(p, pre, blockIdx.x, sg)) {
-        const int qs = n & 1;
-        if (!mbar_wait(bar(kWBarQFull + qs), (n >> 1) & 1, ctl)) break;
-        const uint32_t qb = sb + L.q + qs * 2 * kQHalf;
-        if (LIMITS && sg.w < p.W) {
-          // Padding rows of a shorter window may hold anything (a NaN): they become zeros, whose
-          // scores of 0 add 2^(0 - inf) = 0.
-          for (int i = sg.w * p.G * 8; i < p.R * 8; ++i) {
-            reinterpret_cast<uint4*>(base + L.q + qs * 2 * kQHalf)[i] = make_uint4(0u, 0u, 0u, 0u);
-            reinterpret_cast<uint4*>(base + L.q + qs * 2 * kQHalf + kQHalf)[i] = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_async_smem();
-        }
+    int g = 0, n = 0;
+    bool ok = true;
+    while (ok && it.next<true>(p, pre, blockIdx.x, sg)) {
+      const int qs = n & 1;
+      if (lane == 0) ok = mbar_wait(bar(kWBarQFull + qs), (n >> 1) & 1, ctl);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      const uint32_t qb = sb + L.q + qs * 2 * kQHalf;
+      if (LIMITS && sg.w < p.W) {
+        // Padding rows of a shorter window may hold anything (a NaN): the warp makes them zeros, whose
+        // scores of 0 add 2^(0 - inf) = 0.
+        uint4* q0 = reinterpret_cast<uint4*>(base + L.q + qs * 2 * kQHalf);
+        for (int i = sg.w * p.G * 8 + lane; i < p.R * 8; i += 32)
+          q0[i] = q0[i + kQHalf / 16] = make_uint4(0u, 0u, 0u, 0u);
+        fence_async_smem();
+        __syncwarp();
+      }
+      if (lane == 0) {
         for (int jt = sg.j0; jt < sg.j1; jt += kTileKeys, ++g) {
-          const int ks = g % kWStages, s = g % kWSBufs;
-          if (!mbar_wait(bar(kWBarKFull + ks), (g / kWStages) & 1, ctl) ||
+          const int ks = g % stages, s = g % kWSBufs;
+          if (!mbar_wait(bar(kWBarKFull + ks), (g / stages) & 1, ctl) ||
               (g >= kWSBufs && !mbar_wait(bar(kWBarSEmpty + s), (g / kWSBufs - 1) & 1, ctl))) {
             ok = false;
             break;
@@ -220,8 +226,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
           umma_commit(bar(kWBarKEmpty + ks));
         }
         if (ok) umma_commit(bar(kWBarQEmpty + qs));
-        ++n;
       }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ++n;
+    }
+    if (lane == 0) {
       umma_commit(bar(kWBarDrain));
       mbar_drain(bar(kWBarDrain), 0, 100000000LL);
     }
@@ -229,10 +238,11 @@ __global__ void __launch_bounds__(kWThreads, 1)
     // ------------------------------------------------------------------ sums
     // Each warp keeps its own copy of a segment's row statistics: the warps share no barrier, so
     // one that gives up keeps no other waiting.
-    const int sub = warp & 3, row = 32 * sub + lane;
+    const int sub = warp & 3, row = 32 * sub + lane, group = warp >= 6;
     const uint32_t lane_addr = tmem + ((uint32_t)(32 * sub) << 16);
-    float* lse = reinterpret_cast<float*>(base + L.lse) + sub * NQ;
-    int* lim = reinterpret_cast<int*>(base + L.lim) + sub * NQ;
+    float* lse = reinterpret_cast<float*>(base + L.lse) + (warp - 2) * NQ;
+    int* lim = reinterpret_cast<int*>(base + L.lim) + (warp - 2) * NQ;
+    const uint32_t old_s = sb + (uint32_t)(L.old + group * kAhead * 512 + 4 * row);   // [kAhead][128]
     const float c2 = p.scale_log2;
     pdl_wait();   // the merge (and so the attention) kernel is complete: lse2
     int g = 0;
@@ -248,50 +258,75 @@ __global__ void __launch_bounds__(kWThreads, 1)
       }
       __syncwarp();
       // Window rows start afresh: their slots may hold the weight of an earlier occupant. The old
-      // weights are read kAhead tiles ahead (a tile takes less time than a read).
+      // weights are copied to shared memory kAhead tiles ahead, each lane its own (a tile takes less
+      // time than a read, and a register with a read in flight cannot be passed on).
       const int old_end = kw.in ? min(sg.n - sg.w, sg.j1) : 0;
-      auto old_at = [&](int key) { return key < old_end ? kw.in[head * p.S + key] : 0.f; };
-      float ahead[kAhead];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) ahead[i] = old_at(sg.j0 + row + i * kTileKeys);
-      for (int jt = sg.j0; jt < sg.j1; jt += kTileKeys, ++g) {
-        const int key = jt + row, s = g % kWSBufs;
+      auto read_ahead = [&](int key, int slot) {   // zero where there is no old weight
+        const float* src = key < old_end ? kw.in + head * p.S + key : kw.out;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(old_s + (uint32_t)slot * 512u), "l"(src),
+                     "r"(key < old_end ? 4 : 0)
+                     : "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      // This group's tiles of the segment: every other one of the CTA's.
+      const int skip = (g ^ group) & 1, tiles = (sg.j1 - sg.j0 + kTileKeys - 1) / kTileKeys;
+      const int g0 = g;
+      g += tiles;
+#pragma unroll 1
+      for (int i = 0; i < kAhead; ++i) read_ahead(sg.j0 + row + (skip + 2 * i) * kTileKeys, i);
+#pragma unroll 1
+      for (int t = skip, slot = 0; t < tiles; t += 2, slot = (slot + 1) % kAhead) {
+        const int jt = sg.j0 + t * kTileKeys, gt = g0 + t;
+        const int key = jt + row, s = gt % kWSBufs;
         const bool key_ok = key < sg.j1;
         const bool edge = p.mask_mode != 0 && jt + kTileKeys > sg.n - sg.w;   // rows differ in what they see
-        const float old = ahead[0];
-#pragma unroll
-        for (int i = 0; i + 1 < kAhead; ++i) ahead[i] = ahead[i + 1];
-        ahead[kAhead - 1] = old_at(key + kAhead * kTileKeys);
-        ok = __all_sync(0xffffffffu, mbar_wait(bar(kWBarSFull + s), (g / kWSBufs) & 1, ctl));
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(kWBarSFull + s), (gt / kWSBufs) & 1, ctl));
         if (!ok) break;
         tc_fence_after();
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        constexpr int kChunk = NQ % 48 == 0 ? 48 : NQ % 32 == 0 ? 32 : 16;   // columns held at once
+        constexpr int kChunk = NQ <= 80 ? NQ : 64;   // columns held at once
+        if (LIMITS && edge) {
+          // The last tile or two of a sequence, in little code.
+#pragma unroll 1
+          for (int c = 0; c < NQ; c += 16) {
+            float x[16];
+            tmem_ld16(lane_addr + s * NQ + c, x);
+            tc_wait_ld();
 #pragma unroll
-        for (int c = 0; c < NQ; c += kChunk) {
-          float x[kChunk];
-#pragma unroll
-          for (int e = 0; e < kChunk; e += 16) tmem_ld16(lane_addr + s * NQ + c + e, x + e);
-          tc_wait_ld();
-          if (c + kChunk >= NQ) {
-            tc_fence_before();
-            mbar_arrive(bar(kWBarSEmpty + s));
+            for (int i = 0; i < 16; ++i)
+              sum[i & 3] += key < lim[c + i] ? fast_exp2(fmaf(x[i], c2, -lse[c + i])) : 0.f;
           }
+          tc_fence_before();
+          mbar_arrive(bar(kWBarSEmpty + s));
+        } else {
 #pragma unroll
-          for (int e = 0; e < kChunk; e += 4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(lse + c + e);
-            const float l[4] = {l4.x, l4.y, l4.z, l4.w};
+          for (int c = 0; c < NQ; c += kChunk) {
+            float x[kChunk];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float pr = fast_exp2(fmaf(x[e + i], c2, -l[i]));
-              if (LIMITS && edge) pr = key < lim[c + e + i] ? pr : 0.f;
-              sum[i] += pr;
+            for (int e = 0; e < kChunk && c + e < NQ; e += 16) tmem_ld16(lane_addr + s * NQ + c + e, x + e);
+            tc_wait_ld();
+            if (c + kChunk >= NQ) {
+              tc_fence_before();
+              mbar_arrive(bar(kWBarSEmpty + s));
+            }
+#pragma unroll
+            for (int e = 0; e < kChunk && c + e < NQ; e += 4) {
+              const float4 l = *reinterpret_cast<const float4*>(lse + c + e);
+              sum[0] += fast_exp2(fmaf(x[e], c2, -l.x));
+              sum[1] += fast_exp2(fmaf(x[e + 1], c2, -l.y));
+              sum[2] += fast_exp2(fmaf(x[e + 2], c2, -l.z));
+              sum[3] += fast_exp2(fmaf(x[e + 3], c2, -l.w));
             }
           }
         }
+        float old;
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(old) : "r"(old_s + (uint32_t)slot * 512u) : "memory");
         if (key_ok) kw.out[head * p.S + key] = fmaf(kw.decay, old, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+        read_ahead(key + 2 * kAhead * kTileKeys, slot);
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
 
   tc_fence_before();
@@ -306,12 +341,15 @@ __global__ void __launch_bounds__(kWThreads, 1)
 template <int NQ, bool LIMITS, bool PAGED>
 cudaError_t launch_w(const Problem& p, const KeyWeights& kw, const CUtensorMap& k, const CUtensorMap& q,
                      cudaStream_t s) {
-  const size_t smem = (size_t)1024 + w_layout(NQ, p.B).end;
+  // As deep a K ring as fits (a large batch's plan takes its share of shared memory).
+  int stages = kWMaxStages;
+  while (stages > 2 && 1024 + w_layout(NQ, stages, p.B).end > 227 * 1024) --stages;
+  const size_t smem = (size_t)1024 + w_layout(NQ, stages, p.B).end;
   cudaError_t e = cudaFuncSetAttribute(key_weights_kernel<NQ, LIMITS, PAGED>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(key_weights_kernel<NQ, LIMITS, PAGED>, dim3(p.num_ctas), dim3(kWThreads), smem, s, k, q,
-                    p, kw);
+                    p, kw, stages);
 }
 
 }  // namespace
