@@ -1,7 +1,9 @@
 """Python binding of ``libla_pbd.so``, the B200 PBD window-attention library.
 
 Argument marshalling only: every step of the computation runs in the library's CUDA kernels
-(see ``include/la_pbd.h`` for the C ABI). The functions take torch CUDA tensors for device
+(see ``include/la_pbd.h`` for the C ABI). The attention entry points go through ctypes; the operators
+around them (rotary positions, key weights, eviction, verification), whose kernels are shorter than
+that, through the module ``_la_torch`` (``csrc/torch_binding.cpp``), which makes the same checks. The functions take torch CUDA tensors for device
 memory and use torch's current CUDA stream; they never fall back to another implementation:
 if the shared library is missing or fails to load, they raise.
 """
@@ -580,130 +582,60 @@ def la_rope_plan_init(plan: RopePlan, rotary_dim: int, layout: int, scaling: int
                                     float(high_turns), float(out_scale)), "la_rope_plan_init")
 
 
-def _on_current_device(*tensors) -> None:
-    import torch
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"all tensors must be on the current device (cuda:{dev}), got {t.device}")
+_EXT = None
 
 
-_NUMBERS = {}
+def _ext():
+    """The module over torch tensors (raises if it has not been built)."""
+    global _EXT
+    if _EXT is None:
+        load()
+        try:
+            from . import _la_torch
+        except ImportError as e:
+            raise RuntimeError(f"{os.path.join(_HERE, '_la_torch.so')} is missing or does not load: build "
+                               "it with `python -m block_masked_window_b200.build`") from e
+        _EXT = _la_torch
+    return _EXT
 
 
-def _dtype_number(t, name) -> int:
-    if not _NUMBERS:
-        import torch
-        _NUMBERS.update({torch.bfloat16: LA_DTYPE_BF16, torch.float16: LA_DTYPE_F16,
-                         torch.float32: LA_DTYPE_F32})
-    if t.dtype not in _NUMBERS:
-        raise TypeError(f"{name}: expected bf16, fp16 or fp32, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor")
-    return _NUMBERS[t.dtype]
+_address = ctypes.addressof
+
+
+def _handle(stream):
+    """None (the current stream), or a stream's handle."""
+    return stream if stream is None or isinstance(stream, int) else int(stream.cuda_stream)
 
 
 def la_rope(plan: RopePlan, x, positions, out, inverse: bool = False, stream=None) -> None:
     """out = x turned by position: x, out [T, H, D] (bf16, fp16 or fp32, channels contiguous),
     positions int32 [T]. `inverse` turns back: the gradient of x from the gradient of out."""
-    num = _dtype_number(x, "x")
-    if x.dim() != 3 or out.shape != x.shape or out.dtype is not x.dtype:
-        raise ValueError(f"x, out: expected [T, H, D] of one shape and type, got {tuple(x.shape)} "
-                         f"{x.dtype} and {tuple(out.shape)} {out.dtype}")
-    T, H, D = x.shape
-    if D > 1 and (x.stride(2) != 1 or out.stride(2) != 1):
-        raise ValueError("x, out: channels must be contiguous")
-    _check_tensor(positions, "positions", "i32", (T,))
-    _on_current_device(x, positions, out)
-    _check(load().la_rope(ctypes.byref(plan), num, x.data_ptr(), x.stride(0), x.stride(1),
-                          positions.data_ptr(), T, H, D, 1 if inverse else 0, out.data_ptr(),
-                          out.stride(0), out.stride(1), _stream(stream)), "la_rope")
-
-
-def _token_stride(t, name, shape) -> int:
-    """Elements between consecutive rows of a [B, T, H, D] tensor whose heads are dense and whose
-    batch is evenly strided (a part of a fused projection's output, or contiguous)."""
-    _check_dtype_cuda(t, name)
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    B, T, H, D = shape
-    st = t.stride()
-    tok = st[1] if T > 1 else st[0] if B > 1 else H * D
-    if st[3] != 1 or (H > 1 and st[2] != D) or (B > 1 and st[0] != T * tok):
-        raise ValueError(f"{name}: heads must be dense and rows evenly strided, got strides {st}")
-    return tok
-
-
-def _check_dtype_cuda(t, name):
-    import torch
-    if t.dtype is not torch.bfloat16:
-        raise TypeError(f"{name}: expected bf16, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor")
-
-
-def _append_strides(cfg, q, k_new, v_new, seq_lens, row_lens, pos0, q_out, key_pos, slots):
-    B, Hq, Hkv, D = cfg.batch, cfg.num_q_heads, cfg.num_kv_heads, cfg.head_dim
-    if q.dim() != 4:
-        raise ValueError(f"q: expected [B, T, Hq, D], got {tuple(q.shape)}")
-    T = int(q.shape[1])
-    strides = (_token_stride(q, "q", (B, T, Hq, D)), _token_stride(k_new, "k_new", (B, T, Hkv, D)),
-               _token_stride(v_new, "v_new", (B, T, Hkv, D)))
-    _check_tensor(q_out, "q_out", "bf16", (B, T, Hq, D))
-    for name, t in (("seq_lens", seq_lens), ("row_lens", row_lens), ("pos0", pos0)):
-        if t is not None:
-            _check_tensor(t, name, "i32", (B,))
-    if key_pos is not None:
-        _check_tensor(key_pos, "key_pos", "i32", (B, Hkv, slots))
-    return T, strides
+    st = _ext().rope(_address(plan), x, positions, out, 1 if inverse else 0, _handle(stream))
+    if st:
+        _check(st, "la_rope")
 
 
 def la_rope_append(cfg: Config, plan: RopePlan, q, k_new, v_new, seq_lens, q_out, k_cache, v_cache,
                    row_lens=None, pos0=None, key_pos=None, stream=None) -> None:
     """Rotate the rows of a window or a prompt and append them: q [B, T, Hq, D] into q_out, k_new
     [B, T, Hkv, D] into cache rows P_b + i, v_new copied there, positions into key_pos. seq_lens
-    None: P_b = 0; pos0 None: positions start at P_b."""
-    T, (sq, sk, sv) = _append_strides(cfg, q, k_new, v_new, seq_lens, row_lens, pos0, q_out, key_pos,
-                                      cfg.max_seq)
-    cache = (cfg.batch, cfg.num_kv_heads, cfg.max_seq, cfg.head_dim)
-    _check_tensor(k_cache, "k_cache", "bf16", cache)
-    _check_tensor(v_cache, "v_cache", "bf16", cache)
-    _on_current_device(q, k_new, v_new, seq_lens, q_out, k_cache, v_cache, row_lens, pos0, key_pos)
-    _check(load().la_rope_append(ctypes.byref(cfg), ctypes.byref(plan), q.data_ptr(), sq,
-                                 k_new.data_ptr(), sk, v_new.data_ptr(), sv, _ptr(seq_lens),
-                                 _ptr(row_lens), _ptr(pos0), T, q_out.data_ptr(), k_cache.data_ptr(),
-                                 v_cache.data_ptr(), _ptr(key_pos), _stream(stream)),
-           "la_rope_append")
-
-
-def _pool(cfg, k_pool, v_pool, block_table):
-    """(num_pages, page_size, pages_per_seq) of checked page pools and their table."""
-    _check_tensor(k_pool, "k_pool", "bf16")
-    _check_tensor(v_pool, "v_pool", "bf16", k_pool.shape)
-    if k_pool.dim() != 4 or k_pool.shape[1] != cfg.num_kv_heads or k_pool.shape[3] != cfg.head_dim:
-        raise ValueError(f"k_pool: expected [num_pages, {cfg.num_kv_heads}, page_size, "
-                         f"{cfg.head_dim}], got {tuple(k_pool.shape)}")
-    _check_tensor(block_table, "block_table", "i32")
-    if block_table.dim() != 2 or block_table.shape[0] != cfg.batch:
-        raise ValueError(f"block_table: expected [{cfg.batch}, pages_per_seq], got "
-                         f"{tuple(block_table.shape)}")
-    return int(k_pool.shape[0]), int(k_pool.shape[2]), int(block_table.shape[1])
+    None: P_b = 0; pos0 None: positions start at P_b. q, k_new and v_new may be parts of one
+    projection's output."""
+    st = _ext().rope_append(_address(cfg), _address(plan), q, k_new, v_new, None, seq_lens, q_out, k_cache,
+                            v_cache, row_lens, pos0, key_pos, _handle(stream))
+    if st:
+        _check(st, "la_rope_append")
 
 
 def la_rope_append_paged(cfg: Config, plan: RopePlan, q, k_new, v_new, block_table, seq_lens, q_out,
                          k_pool, v_pool, row_lens=None, pos0=None, key_pos=None, stream=None) -> None:
     """la_rope_append into paged caches (pools and table as in la_pbd_attn_paged)."""
-    pages, size, pps = _pool(cfg, k_pool, v_pool, block_table)
-    T, (sq, sk, sv) = _append_strides(cfg, q, k_new, v_new, seq_lens, row_lens, pos0, q_out, key_pos,
-                                      pps * size)
-    _on_current_device(q, k_new, v_new, block_table, seq_lens, q_out, k_pool, v_pool, row_lens, pos0,
-                       key_pos)
-    _check(load().la_rope_append_paged(ctypes.byref(cfg), ctypes.byref(plan), q.data_ptr(), sq,
-                                       k_new.data_ptr(), sk, v_new.data_ptr(), sv,
-                                       block_table.data_ptr(), pps, size, pages, _ptr(seq_lens),
-                                       _ptr(row_lens), _ptr(pos0), T, q_out.data_ptr(),
-                                       k_pool.data_ptr(), v_pool.data_ptr(), _ptr(key_pos),
-                                       _stream(stream)), "la_rope_append_paged")
+    if block_table is None:
+        raise TypeError("block_table: expected a tensor, got None")
+    st = _ext().rope_append(_address(cfg), _address(plan), q, k_new, v_new, block_table, seq_lens, q_out,
+                            k_pool, v_pool, row_lens, pos0, key_pos, _handle(stream))
+    if st:
+        _check(st, "la_rope_append_paged")
 
 
 # ---------------------------------------------------------------- key weights and eviction
@@ -735,71 +667,27 @@ class EvictWorkspace(Workspace):
         super().__init__(cfg, 1, device=device, nbytes=n)
 
 
-def _check_weights(cfg, W, slots, q, seq_lens, out, weights_in, weights_out, window_lens):
-    q_shape = (cfg.batch, W, cfg.num_q_heads, cfg.head_dim)
-    w_shape = (cfg.batch, cfg.num_kv_heads, slots)
-    _check_tensor(q, "q", "bf16", q_shape)
-    _check_tensor(seq_lens, "seq_lens", "i32", (cfg.batch,))
-    _check_tensor(out, "out", "bf16", q_shape)
-    _check_tensor(weights_out, "weights_out", "f32", w_shape)
-    if weights_in is not None:
-        _check_tensor(weights_in, "weights_in", "f32", w_shape)
-    if window_lens is not None:
-        _check_tensor(window_lens, "window_lens", "i32", (cfg.batch,))
-
-
 def la_pbd_attn_weights(cfg: Config, q, k_cache, v_cache, seq_lens, window_len: int, out, weights_out,
                         workspace: Workspace, weights_in=None, decay: float = 1.0, window_lens=None,
                         stream=None) -> None:
     """Window attention that also adds each key's attention weight, summed over the rows that share
     its KV head, to decay * weights_in: weights fp32 [B, Hkv, S_max]."""
-    W = int(window_len)
-    _check_weights(cfg, W, cfg.max_seq, q, seq_lens, out, weights_in, weights_out, window_lens)
-    cache = (cfg.batch, cfg.num_kv_heads, cfg.max_seq, cfg.head_dim)
-    _check_tensor(k_cache, "k_cache", "bf16", cache)
-    _check_tensor(v_cache, "v_cache", "bf16", cache)
-    _on_current_device(q, k_cache, v_cache, seq_lens, out, weights_out, weights_in, window_lens,
-                       workspace.tensor)
-    _check(load().la_pbd_attn_weights(ctypes.byref(cfg), q.data_ptr(), k_cache.data_ptr(),
-                                      v_cache.data_ptr(), seq_lens.data_ptr(), _ptr(window_lens), W,
-                                      out.data_ptr(), _ptr(weights_in), float(decay),
-                                      weights_out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-                                      _stream(stream)), "la_pbd_attn_weights")
+    st = _ext().attn_weights(_address(cfg), q, k_cache, v_cache, None, seq_lens, window_len, out, weights_out,
+                             workspace.tensor, weights_in, decay, window_lens, _handle(stream))
+    if st:
+        _check(st, "la_pbd_attn_weights")
 
 
 def la_pbd_attn_weights_paged(cfg: Config, q, k_pool, v_pool, block_table, seq_lens, window_len: int,
                               out, weights_out, workspace: Workspace, weights_in=None,
                               decay: float = 1.0, window_lens=None, stream=None) -> None:
     """la_pbd_attn_weights over paged caches; weights [B, Hkv, pages_per_seq * page_size]."""
-    W = int(window_len)
-    pages, size, pps = _pool(cfg, k_pool, v_pool, block_table)
-    _check_weights(cfg, W, pps * size, q, seq_lens, out, weights_in, weights_out, window_lens)
-    _on_current_device(q, k_pool, v_pool, block_table, seq_lens, out, weights_out, weights_in,
-                       window_lens, workspace.tensor)
-    _check(load().la_pbd_attn_weights_paged(ctypes.byref(cfg), q.data_ptr(), k_pool.data_ptr(),
-                                            v_pool.data_ptr(), block_table.data_ptr(), pps, size,
-                                            pages, seq_lens.data_ptr(), _ptr(window_lens), W,
-                                            out.data_ptr(), _ptr(weights_in), float(decay),
-                                            weights_out.data_ptr(), workspace.data_ptr(),
-                                            workspace.nbytes, _stream(stream)),
-           "la_pbd_attn_weights_paged")
-
-
-def _check_evict(cfg, slots, budget, weights, seq_lens, weights_out, new_lens, key_pos, next_pos,
-                 key_pos_out, kept_slots):
-    B, Hkv = cfg.batch, cfg.num_kv_heads
-    _check_tensor(weights, "weights", "f32", (B, Hkv, slots))
-    _check_tensor(weights_out, "weights_out", "f32", (B, Hkv, slots))
-    _check_tensor(seq_lens, "seq_lens", "i32", (B,))
-    _check_tensor(new_lens, "new_lens", "i32", (B,))
-    if key_pos is not None:
-        _check_tensor(key_pos, "key_pos", "i32", (B, Hkv, slots))
-    if key_pos_out is not None:
-        _check_tensor(key_pos_out, "key_pos_out", "i32", (B, Hkv, slots))
-    if next_pos is not None:
-        _check_tensor(next_pos, "next_pos", "i32", (B,))
-    if kept_slots is not None:
-        _check_tensor(kept_slots, "kept_slots", "i32", (B, Hkv, budget))
+    if block_table is None:
+        raise TypeError("block_table: expected a tensor, got None")
+    st = _ext().attn_weights(_address(cfg), q, k_pool, v_pool, block_table, seq_lens, window_len, out,
+                             weights_out, workspace.tensor, weights_in, decay, window_lens, _handle(stream))
+    if st:
+        _check(st, "la_pbd_attn_weights_paged")
 
 
 def la_kv_evict(cfg: Config, weights, seq_lens, budget: int, k_cache, v_cache, weights_out, new_lens,
@@ -808,19 +696,11 @@ def la_kv_evict(cfg: Config, weights, seq_lens, budget: int, k_cache, v_cache, w
     """Bring every sequence down to min(P_b, budget) keys per KV head: protected positions (the first
     `sink`, the last `recent`) and the highest weights stay; kept keys beyond the new length move
     into the evicted slots. The caches are changed in place."""
-    budget = int(budget)
-    _check_evict(cfg, cfg.max_seq, budget, weights, seq_lens, weights_out, new_lens, key_pos, next_pos,
-                 key_pos_out, kept_slots)
-    cache = (cfg.batch, cfg.num_kv_heads, cfg.max_seq, cfg.head_dim)
-    _check_tensor(k_cache, "k_cache", "bf16", cache)
-    _check_tensor(v_cache, "v_cache", "bf16", cache)
-    _on_current_device(weights, seq_lens, k_cache, v_cache, weights_out, new_lens, key_pos, next_pos,
-                       key_pos_out, kept_slots, workspace.tensor)
-    _check(load().la_kv_evict(ctypes.byref(cfg), weights.data_ptr(), _ptr(key_pos), seq_lens.data_ptr(),
-                              _ptr(next_pos), budget, int(sink), int(recent), k_cache.data_ptr(),
-                              v_cache.data_ptr(), weights_out.data_ptr(), _ptr(key_pos_out),
-                              _ptr(kept_slots), new_lens.data_ptr(), workspace.data_ptr(),
-                              workspace.nbytes, _stream(stream)), "la_kv_evict")
+    st = _ext().kv_evict(_address(cfg), weights, None, seq_lens, budget, k_cache, v_cache, weights_out, new_lens,
+                         workspace.tensor, key_pos, next_pos, sink, recent, key_pos_out, kept_slots,
+                         _handle(stream))
+    if st:
+        _check(st, "la_kv_evict")
 
 
 def la_kv_evict_paged(cfg: Config, weights, block_table, seq_lens, budget: int, k_pool, v_pool,
@@ -829,18 +709,13 @@ def la_kv_evict_paged(cfg: Config, weights, block_table, seq_lens, budget: int, 
                       stream=None) -> None:
     """la_kv_evict over paged caches (the workspace of a cfg with max_seq = pages_per_seq *
     page_size)."""
-    budget = int(budget)
-    pages, size, pps = _pool(cfg, k_pool, v_pool, block_table)
-    _check_evict(cfg, pps * size, budget, weights, seq_lens, weights_out, new_lens, key_pos, next_pos,
-                 key_pos_out, kept_slots)
-    _on_current_device(weights, block_table, seq_lens, k_pool, v_pool, weights_out, new_lens, key_pos,
-                       next_pos, key_pos_out, kept_slots, workspace.tensor)
-    _check(load().la_kv_evict_paged(ctypes.byref(cfg), weights.data_ptr(), _ptr(key_pos),
-                                    block_table.data_ptr(), pps, size, pages, seq_lens.data_ptr(),
-                                    _ptr(next_pos), budget, int(sink), int(recent), k_pool.data_ptr(),
-                                    v_pool.data_ptr(), weights_out.data_ptr(), _ptr(key_pos_out),
-                                    _ptr(kept_slots), new_lens.data_ptr(), workspace.data_ptr(),
-                                    workspace.nbytes, _stream(stream)), "la_kv_evict_paged")
+    if block_table is None:
+        raise TypeError("block_table: expected a tensor, got None")
+    st = _ext().kv_evict(_address(cfg), weights, block_table, seq_lens, budget, k_pool, v_pool, weights_out,
+                         new_lens, workspace.tensor, key_pos, next_pos, sink, recent, key_pos_out, kept_slots,
+                         _handle(stream))
+    if st:
+        _check(st, "la_kv_evict_paged")
 
 
 # ---------------------------------------------------------------- draft verification
@@ -849,28 +724,7 @@ def la_pbd_verify(p, q, drafts, u, sample_u, tokens, accepted, draft_lens=None, 
     """Accept drafted tokens against the target's probabilities and draw the next one, from given
     uniforms: p [B, K + 1, V], q [B, K, V] or None (bf16, fp16 or fp32, entries contiguous), drafts
     int32 [B, K], u fp32 [B, K], sample_u fp32 [B], tokens int32 [B, K + 1], accepted int32 [B]."""
-    num = _dtype_number(p, "p")
-    if p.dim() != 3 or p.shape[1] < 1 or (p.shape[2] > 1 and p.stride(2) != 1):
-        raise ValueError(f"p: expected [B, K + 1, V] with contiguous entries, got {tuple(p.shape)} "
-                         f"strides {p.stride()}")
-    B, K, V = p.shape
-    K -= 1
-    qb = qr = 0
-    if q is not None:
-        if q.dtype is not p.dtype or not q.is_cuda or q.shape != (B, K, V) or (V > 1 and q.stride(2) != 1):
-            raise ValueError(f"q: expected [{B}, {K}, {V}] of {p.dtype} with contiguous entries, got "
-                             f"{tuple(q.shape)} {q.dtype} strides {q.stride()}")
-        qb, qr = q.stride(0), q.stride(1)
-    _check_tensor(drafts, "drafts", "i32", (B, K))
-    _check_tensor(u, "u", "f32", (B, K))
-    _check_tensor(sample_u, "sample_u", "f32", (B,))
-    _check_tensor(tokens, "tokens", "i32", (B, K + 1))
-    _check_tensor(accepted, "accepted", "i32", (B,))
-    for name, t in (("draft_lens", draft_lens), ("seq_lens", seq_lens), ("seq_lens_out", seq_lens_out)):
-        if t is not None:
-            _check_tensor(t, name, "i32", (B,))
-    _on_current_device(p, q, drafts, u, sample_u, tokens, accepted, draft_lens, seq_lens, seq_lens_out)
-    _check(load().la_pbd_verify(num, p.data_ptr(), p.stride(0), p.stride(1), _ptr(q), qb, qr,
-                                drafts.data_ptr(), _ptr(draft_lens), u.data_ptr(), sample_u.data_ptr(),
-                                B, K, V, tokens.data_ptr(), accepted.data_ptr(), _ptr(seq_lens),
-                                _ptr(seq_lens_out), _stream(stream)), "la_pbd_verify")
+    st = _ext().verify(p, q, drafts, u, sample_u, tokens, accepted, draft_lens, seq_lens, seq_lens_out,
+                       _handle(stream))
+    if st:
+        _check(st, "la_pbd_verify")

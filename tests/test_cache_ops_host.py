@@ -220,6 +220,14 @@ def test_binding_refusals(lib):
         bmw.la_pbd_verify(torch.zeros(1, 2, 8, dtype=torch.float64), None, *(torch.zeros(1, 1),) * 5)
     with pytest.raises(bmw.LaError):
         bmw.EvictWorkspace(_cfg(head_dim=64))
+    with pytest.raises(TypeError):
+        bmw.la_rope(plan, None, None, None)
+    with pytest.raises(TypeError):
+        bmw.la_rope_append_paged(cfg, plan, q, q, q, None, None, q, q, q)
+    with pytest.raises(TypeError):
+        bmw.la_pbd_attn_weights_paged(cfg, q, q, q, None, q, 6, q, q, None)
+    with pytest.raises(TypeError):
+        bmw.la_kv_evict_paged(cfg, q, None, q, 6, q, q, q, q, None)
 
 
 def test_oracle_rotation_properties():
