@@ -478,7 +478,9 @@ size_t la_pbd_attn_weights_workspace_bytes(const la_pbd_cfg* cfg, int32_t window
  *   weights_in, weights_out  device fp32 [B, Hkv, S_max]; the two may be the same buffer
  *   window_lens              device int32 [B], or NULL: all window_len
  *   workspace                la_pbd_attn_weights_workspace_bytes, header zeroed once
- * A sequence that la_pbd_attn flags keeps its weights. The paged form is for la_pbd_attn_paged's
+ * A sequence that la_pbd_attn flags keeps its weights. Calls whose executions may overlap (other
+ * streams, graphs replayed at the same time) need workspaces of their own, as for la_pbd_attn. The
+ * paged form is for la_pbd_attn_paged's
  * configurations, with window_lens as well; S_max of the weights is pages_per_seq * page_size.
  */
 la_status la_pbd_attn_weights(const la_pbd_cfg* cfg, const void* q, const void* k_cache,
@@ -518,8 +520,8 @@ size_t la_kv_evict_workspace_bytes(const la_pbd_cfg* cfg);
  *   budget                 1 .. S_max, sink + recent <= budget
  *   workspace              la_kv_evict_workspace_bytes, 256-byte aligned, header zeroed once by
  *                          la_pbd_workspace_init
- * Buffers that are not said to be allowed the same may not overlap. With separate outputs the call
- * can be repeated with the same result. A sequence with P_b < 0 or P_b > S_max keeps its cache and
+ * No other two buffers may overlap, and calls whose executions may overlap need workspaces of their
+ * own. With separate outputs the call can be repeated with the same result. A sequence with P_b < 0 or P_b > S_max keeps its cache and
  * length and raises the sticky flag (la_pbd_check). The paged form moves rows between the
  * sequence's own pages, which no other sequence may share; a row whose table entry names no page of
  * the pool is not moved.
@@ -542,7 +544,8 @@ la_status la_kv_evict_paged(const la_pbd_cfg* cfg, const float* weights, const i
  * n_b is the number accepted before the first miss. The next token is drawn from max(p_n - q_n, 0)
  * after a miss (from p_n if that is zero everywhere), from p_n when all were accepted: the smallest
  * j whose cumulative sum exceeds sample_u[b] times the total (the last entry with any weight if
- * none does). Sums and comparisons in 64 bits; entries that are negative or NaN count as 0.
+ * none does). Sums and comparisons in 64 bits; what is to be summed counts as 0 where it is negative
+ * or NaN, and a test against a NaN is a miss.
  *   p            [B, num_drafts + 1, vocab] of `dtype`, entries contiguous, strides in elements
  *   q            [B, num_drafts, vocab] likewise, or NULL: the drafts are certain (q_i(x_i) = 1)
  *   drafts       device int32 [B, num_drafts]; one outside [0, vocab) is a miss
@@ -553,6 +556,7 @@ la_status la_kv_evict_paged(const la_pbd_cfg* cfg, const float* weights, const i
  *   seq_lens, seq_lens_out  device int32 [B], both or neither NULL, may be the same buffer:
  *                seq_lens_out = seq_lens + n_b + 1 (the window's first row, the last accepted token,
  *                and the n_b accepted drafts are now committed)
+ * No other two buffers may overlap. The call has no workspace: calls on any streams are independent.
  * num_drafts 0 .. 32 (0: a draw from p alone), vocab <= 2^24. k_b outside [0, num_drafts] gives
  * accepted = -1, tokens -1 and the length unchanged; a row whose sum is zero or not finite
  * gives -1 for the drawn token.
