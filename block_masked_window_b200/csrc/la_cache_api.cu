@@ -129,7 +129,9 @@ la_status la_rope(const la_rope_plan* plan, int32_t dtype, const void* x, int64_
   p.heads = heads;
   p.head_dim = head_dim;
   p.inverse = inverse != 0;
-  return la::launch_rope(*plan, p, dtype, (cudaStream_t)stream) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
+  int sms = 0;
+  if (la::sm_count(&sms) != cudaSuccess) return LA_ERR_CUDA;
+  return la::launch_rope(*plan, p, dtype, sms, (cudaStream_t)stream) == cudaSuccess ? LA_OK : LA_ERR_CUDA;
 }
 
 }  // extern "C"

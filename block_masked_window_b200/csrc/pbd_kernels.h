@@ -77,7 +77,8 @@ struct RopeProblem {
   int heads, head_dim;
   bool inverse;
 };
-cudaError_t launch_rope(const la_rope_plan& plan, const RopeProblem& p, int dtype, cudaStream_t stream);
+cudaError_t launch_rope(const la_rope_plan& plan, const RopeProblem& p, int dtype, int sms,
+                        cudaStream_t stream);
 
 // Rotation and append of T rows a sequence.
 struct RopeAppendProblem {

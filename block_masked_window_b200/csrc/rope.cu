@@ -10,7 +10,9 @@
 // Angles: f_i is handed to the kernels as a 64-bit fraction of a turn, so that t f_i modulo a turn is
 // one wrapping integer product (error below 2^-33 turns at t = 2^31; in 64-bit floating point the
 // product, its reduction and the conversions took a third of the kernel's instructions). Its upper
-// 32 bits become half turns in [-1, 1), of which sine and cosine are taken in 32 bits. A block computes the
+// 32 bits become half turns in [-1, 1), of which sine and cosine are taken in 32 bits: with full
+// accuracy for fp32 results, and for 16-bit ones, whose rounding is 2^-12 of the value at best, with the
+// fast functions (2^-21 absolute). A block computes the
 // cosines and sines of its tokens once into shared memory; every head of those tokens uses
 // them, so the transcendental work is 1/(heads) of the elements.
 //
@@ -26,9 +28,11 @@ namespace la {
 namespace {
 
 constexpr int kMaxPairs = 128;
-constexpr int kRopeThreads = 256;
-// Items whose loads a thread keeps in flight: 128 bytes, with registers for four blocks an SM.
-template <typename E> constexpr int kItemsOf = sizeof(E) == 4 ? 2 : 4;
+constexpr int kRopeThreads = 128;
+// Blocks per SM: as many as keep the kernel's registers.
+constexpr int rope_ctas(bool half) { return half ? 7 : 6; }
+// Items whose loads a thread keeps in flight: 64 bytes.
+template <typename E> constexpr int kItemsOf = sizeof(E) == 4 ? 1 : 2;
 
 template <typename E> struct Vec8;
 template <> struct Vec8<float> {
@@ -117,26 +121,57 @@ Turns turns_of(const la_rope_plan& pl, bool inverse) {
 }
 
 // (scaled cosine, scaled sine) at position t of a pair that turns by the fraction f per position.
+template <bool EXACT>
 __device__ __forceinline__ float2 turn_at(unsigned long long f, float scale, float sign, long long t) {
   const int half = (int)((f * (unsigned long long)t) >> 32);         // of a turn, times 2^32
   float s, c;
-  sincospif((float)half * 4.656612873077393e-10f, &s, &c);           // 2^-31: half turns
+  if (EXACT) {
+    sincospif((float)half * 4.656612873077393e-10f, &s, &c);         // 2^-31: half turns
+  } else {
+    const float x = (float)half * 1.4629180792671596e-9f;            // 2^-31 pi: in [-pi, pi]
+    s = __sinf(x);
+    c = __cosf(x);
+  }
   return make_float2(c * scale, s * scale * sign);
 }
 
-// Cosines and sines of a token are kept as a float4 (cos, cos, sin, sin) for two pairs, pairs 8s + 2e
-// and 8s + 2e + 1 of item s at [e][s]: neighbouring items (lanes) then read neighbouring 16-byte words,
-// and two pairs are turned by one packed instruction. rot = items that hold pairs.
-__device__ __forceinline__ void table_put(float* table, int pair, int rot, float2 cs) {
-  float* at = table + 4 * (((pair & 7) >> 1) * rot + (pair >> 3)) + (pair & 1);
-  at[0] = cs.x;
-  at[2] = cs.y;
+// What a thread handles at a time: item s of a head, two chunks of 8 channels, so that neighbouring lanes
+// move neighbouring chunks (16 channels in one piece would leave every memory instruction with half of
+// each sector). Half layout: pairs 8s .. 8s + 7, their first and second channels (items past the pairs
+// hold channels that are copied). Interleaved: channels 8s on and head_dim / 2 + 8s on, that is pairs 4s
+// .. 4s + 3 and head_dim / 4 + 4s .. + 3.
+template <bool HALF>
+__device__ __forceinline__ int pair_of(int s, int e, int head_dim) {
+  return HALF ? 8 * s + e : e < 4 ? 4 * s + e : (head_dim >> 2) + 4 * s + e - 4;
 }
+// The item's chunks, and whether any of its pairs turns.
+template <bool HALF>
+__device__ __forceinline__ bool item_chunks(int s, int pairs, int head_dim, int* ca, int* cb) {
+  if (HALF) {
+    const int rot = pairs >> 3;          // items that hold pairs (pairs % 8 == 0)
+    if (s < rot) {
+      *ca = 8 * s;
+      *cb = 8 * s + pairs;
+      return true;
+    }
+    *ca = 2 * pairs + 16 * (s - rot);
+    *cb = *ca + 8;
+    return false;
+  }
+  *ca = 8 * s;
+  *cb = *ca + (head_dim >> 1);
+  return 4 * s < pairs;
+}
+
+// Cosines and sines of an item's eight pairs, two pairs to a float4 (cos, cos, sin, sin), so that two are
+// turned by one packed instruction. In a table of a token (items of 128 channels) the float4 of pairs
+// 2e and 2e + 1 of item s lies at [e][s]: neighbouring lanes read neighbouring words.
+constexpr int kItemsOfHead = kHeadDim / 16;
 struct Turn8 {
   float4 cs[4];
-  __device__ __forceinline__ void load(const float* table, int s, int rot) {
+  __device__ __forceinline__ void load(const float* table, int s) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) cs[e] = reinterpret_cast<const float4*>(table)[e * rot + s];
+    for (int e = 0; e < 4; ++e) cs[e] = reinterpret_cast<const float4*>(table)[e * kItemsOfHead + s];
   }
   __device__ __forceinline__ float cos_of(int e) const { return (e & 1) ? cs[e >> 1].y : cs[e >> 1].x; }
   __device__ __forceinline__ float sin_of(int e) const { return (e & 1) ? cs[e >> 1].w : cs[e >> 1].z; }
@@ -159,11 +194,10 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return d;
 }
 
-// Rotates the 16 channels of one item, pairs i0 .. i0 + 7. Half layout: a and b hold the pairs'
-// first and second channels. Interleaved: a holds pairs i0 .. i0 + 3 and b the next four;
-// pairs from `pairs` on are copied.
+// Rotates the 16 channels of item `s`; pairs from `pairs` on are copied.
 template <bool HALF, typename E>
-__device__ __forceinline__ void rotate_item(Vec8<E>& a, Vec8<E>& b, const Turn8& t, int i0, int pairs) {
+__device__ __forceinline__ void rotate_item(Vec8<E>& a, Vec8<E>& b, const Turn8& t, int s, int pairs,
+                                            int head_dim) {
   float x[8], y[8];
   a.get(x);
   b.get(y);
@@ -180,13 +214,23 @@ __device__ __forceinline__ void rotate_item(Vec8<E>& a, Vec8<E>& b, const Turn8&
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float* z = e < 4 ? x : y;
-      const int k = 2 * (e & 3);
-      if (i0 + e < pairs) {
-        const float c = t.cos_of(e), s = t.sin_of(e), u = z[k], w = z[k + 1];
-        z[k] = fmaf(u, c, -(w * s));
-        z[k + 1] = fmaf(w, c, u * s);
+    for (int half = 0; half < 2; ++half) {
+      float* z = half ? y : x;
+      const int n = pairs - pair_of<false>(s, 4 * half, head_dim);   // of the chunk's pairs that turn
+      if (n >= 4) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float c = t.cos_of(4 * half + e), d = t.sin_of(4 * half + e), u = z[2 * e], w = z[2 * e + 1];
+          z[2 * e] = fmaf(u, c, -(w * d));
+          z[2 * e + 1] = fmaf(w, c, u * d);
+        }
+      } else if (n > 0) {
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+          const float c = t.cos_of(4 * half + e), d = t.sin_of(4 * half + e), u = z[2 * e], w = z[2 * e + 1];
+          z[2 * e] = e < n ? fmaf(u, c, -(w * d)) : u;
+          z[2 * e + 1] = e < n ? fmaf(w, c, u * d) : w;
+        }
       }
     }
   }
@@ -194,77 +238,76 @@ __device__ __forceinline__ void rotate_item(Vec8<E>& a, Vec8<E>& b, const Turn8&
   b.set(y);
 }
 
-// Channel offsets of item s of a head: its two 8-channel chunks and whether they are rotated.
-template <bool HALF>
-__device__ __forceinline__ bool item_chunks(int s, int pairs, int* ca, int* cb) {
-  if (HALF) {
-    const int rot = pairs >> 3;          // items that hold pairs (pairs % 8 == 0)
-    if (s < rot) {
-      *ca = 8 * s;
-      *cb = 8 * s + pairs;
-      return true;
-    }
-    *ca = 2 * pairs + 16 * (s - rot);
-    *cb = *ca + 8;
-    return false;
-  }
-  *ca = 16 * s;
-  *cb = *ca + 8;
-  return 8 * s < pairs;
-}
-
-// ---- Rotation alone: `tok` tokens per block.
+// ---- Rotation alone. A unit of work is `tok` tokens by `hb` heads, one set of items for every
+// thread; blocks stride over the units. What an item is (its token, head, chunks and pairs) is the
+// same in every unit, so its offsets and its 8 fractions stay in registers, and each thread computes
+// its own cosines and sines: 8 of each per 16 channels are within the issue slots that the memory
+// leaves free (about 180 instructions per item against 350), where a table shared by the heads costs a
+// barrier per unit and, with one or two heads, more than it saves (one head of 128, 400000
+// tokens: 204 us with a table).
 template <typename E, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads, 4)
-    rope_kernel(const __grid_constant__ Turns pl, RopeProblem p, int tok) {
-  extern __shared__ __align__(16) float s_table[];   // [tok][16 rot], see table_put
+__global__ void __launch_bounds__(kRopeThreads, rope_ctas(HALF))
+    rope_kernel(const __grid_constant__ Turns pl, RopeProblem p, int tok, int hb) {
+  __shared__ unsigned long long s_f[kMaxPairs];
   constexpr int kItems = kItemsOf<E>;
+  const int pairs = pl.pairs;
   pdl_trigger();
-  pdl_wait();
-  const int pairs = pl.pairs, rot = (pairs + 7) >> 3;
-  const long long t0 = (long long)blockIdx.x * tok;
-  const int nt = (int)min((long long)tok, p.tokens - t0);
+  for (int i = threadIdx.x; i < kMaxPairs; i += kRopeThreads) s_f[i] = i < pairs ? pl.f[i] : 0;
+  __syncthreads();
   const int ns = p.head_dim >> 4;
-  const int per_tok = p.heads * ns;
-  const int total = nt * per_tok;
-  const E* x = static_cast<const E*>(p.x);
-  E* y = static_cast<E*>(p.out);
-  for (int base = threadIdx.x; base < total || base == threadIdx.x; base += kRopeThreads * kItems) {
+  const int nhb = (p.heads + hb - 1) / hb;
+  const long long units = (p.tokens + tok - 1) / tok * nhb;
+  // (The threads past the last whole head of a pass stay idle, so that a thread's items are alike.)
+  const int item = threadIdx.x % ns, pass = kRopeThreads / ns * ns;
+  int ca = 0, cb = 0;
+  const bool turns = item_chunks<HALF>(item, pairs, p.head_dim, &ca, &cb);
+  const int gap = cb - ca;              // distance of the second chunk
+  unsigned long long f[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[e] = s_f[min(pair_of<HALF>(item, e, p.head_dim), kMaxPairs - 1)];
+  long long from[kItems], to[kItems];   // offsets of the item's first chunk in x and out
+  int at[kItems], head[kItems];         // its token (or none) and head in the unit
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const int i = threadIdx.x + k * pass;
+    const int t = i / (hb * ns), h = (i - t * hb * ns) / ns;
+    at[k] = threadIdx.x < pass && t < tok ? t : 1 << 30;
+    head[k] = h;
+    from[k] = t * p.x_tok + h * p.x_head + ca;
+    to[k] = t * p.y_tok + h * p.y_head + ca;
+  }
+  pdl_wait();
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const long long t0 = u / nhb * tok;
+    const int h0 = (int)(u % nhb) * hb;
+    const int nt = (int)min((long long)tok, p.tokens - t0);
+    const E* x = static_cast<const E*>(p.x) + t0 * p.x_tok + (long long)h0 * p.x_head;
+    E* y = static_cast<E*>(p.out) + t0 * p.y_tok + (long long)h0 * p.y_head;
     Vec8<E> a[kItems], b[kItems];
+    int pos[kItems];
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
-      const int it = base + k * kRopeThreads;
-      if (it < total) {
-        const int t = it / per_tok, rem = it - t * per_tok, h = rem / ns, s = rem - h * ns;
-        int ca, cb;
-        item_chunks<HALF>(s, pairs, &ca, &cb);
-        const E* src = x + (t0 + t) * p.x_tok + h * p.x_head;
-        a[k].load(src + ca);
-        b[k].load(src + cb);
+      if (at[k] < nt && h0 + head[k] < p.heads) {
+        a[k].load(x + from[k]);
+        b[k].load(x + from[k] + gap);
+        pos[k] = __ldg(p.positions + t0 + at[k]);
       }
-    }
-    if (base == threadIdx.x) {          // (first pass, every thread)
-      for (int i = threadIdx.x; i < nt * pairs; i += kRopeThreads) {
-        const int t = i / pairs, pair = i - t * pairs;
-        table_put(s_table + t * 16 * rot, pair, rot,
-                  turn_at(pl.f[pair], pl.scale, pl.sign, __ldg(p.positions + t0 + t)));
-      }
-      __syncthreads();
     }
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
-      const int it = base + k * kRopeThreads;
-      if (it < total) {
-        const int t = it / per_tok, rem = it - t * per_tok, h = rem / ns, s = rem - h * ns;
-        int ca, cb;
-        if (item_chunks<HALF>(s, pairs, &ca, &cb)) {
+      if (at[k] < nt && h0 + head[k] < p.heads) {
+        if (turns) {
           Turn8 turn;
-          turn.load(s_table + t * 16 * rot, s, rot);
-          rotate_item<HALF>(a[k], b[k], turn, 8 * s, pairs);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 c0 = turn_at<sizeof(E) == 4>(f[2 * e], pl.scale, pl.sign, pos[k]);
+            const float2 c1 = turn_at<sizeof(E) == 4>(f[2 * e + 1], pl.scale, pl.sign, pos[k]);
+            turn.cs[e] = make_float4(c0.x, c1.x, c0.y, c1.y);
+          }
+          rotate_item<HALF>(a[k], b[k], turn, item, pairs, p.head_dim);
         }
-        E* dst = y + (t0 + t) * p.y_tok + h * p.y_head;
-        a[k].store(dst + ca);
-        b[k].store(dst + cb);
+        a[k].store(y + to[k]);
+        b[k].store(y + to[k] + gap);
       }
     }
   }
@@ -282,7 +325,7 @@ __global__ void __launch_bounds__(kRopeThreads)
   const int nt = (int)min((long long)tok, p.tokens - t0);
   for (int i = threadIdx.x; i < nt * pairs; i += kRopeThreads) {
     const int t = i / pairs;
-    s_cs[i] = turn_at(pl.f[i - t * pairs], pl.scale, pl.sign, __ldg(p.positions + t0 + t));
+    s_cs[i] = turn_at<true>(pl.f[i - t * pairs], pl.scale, pl.sign, __ldg(p.positions + t0 + t));
   }
   __syncthreads();
   const int half = p.head_dim >> 1;
@@ -313,7 +356,8 @@ __global__ void __launch_bounds__(kRopeThreads)
 // l / 8, l / 8 + 4, ... of q, and of k and v, so that the 8 pairs it turns are the same for all of them. The lanes
 // compute two pairs' cosines and sines each, exchange them through the warp's shared memory, and
 // keep their eight in registers. No barrier of the block, no division per item.
-constexpr int kAppendWarps = 4;         // per block
+constexpr int kAppendWarps = 1;         // per block
+constexpr int kAppendCtas = 16;         // blocks per SM (24 warps, with spills: 32.5 us for 16384 tokens, 16: 29.9)
 constexpr int kAppendQ = 4;             // q heads a lane keeps in flight, besides one of k or v
 
 // kWhole: the whole head turns. kPart: part of it. kScalar: no 16-byte chunks (half layout, rotary_dim
@@ -321,7 +365,7 @@ constexpr int kAppendQ = 4;             // q heads a lane keeps in flight, besid
 enum AppendForm { kWhole, kPart, kScalar };
 
 template <bool HALF, AppendForm FORM>
-__global__ void __launch_bounds__(32 * kAppendWarps, 6)
+__global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
     rope_append_kernel(const __grid_constant__ Turns pl, RopeAppendProblem p) {
   using E = __nv_bfloat16;
   __shared__ __align__(16) float s_table[kAppendWarps][kHeadDim];
@@ -329,14 +373,14 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 6)
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float* table = s_table[warp];
-  const int pairs = FORM == kWhole ? kHeadDim / 2 : pl.pairs, rot = (pairs + 7) >> 3;
+  const int pairs = FORM == kWhole ? kHeadDim / 2 : pl.pairs;
   const int heads = p.Hq + 2 * p.Hkv;
   const int s = lane & 7, g = lane >> 3;
-  // The lane's two pairs of the table: the float4 at [g][s] (see table_put).
-  const int own = 8 * s + 2 * g;
+  // The lane's two pairs of the table: the float4 at [g][s] (see Turn8).
+  const int own = pair_of<HALF>(s, 2 * g, kHeadDim);
   const unsigned long long f0 = own < pairs ? pl.f[own] : 0, f1 = own + 1 < pairs ? pl.f[own + 1] : 0;
   int ca, cb;
-  const bool turns = item_chunks<HALF>(s, pairs, &ca, &cb) || FORM == kWhole;
+  const bool turns = item_chunks<HALF>(s, pairs, kHeadDim, &ca, &cb) || FORM == kWhole;
   pdl_wait();
   const int tokens = p.B * p.T, step = gridDim.x * kAppendWarps;
   const bool whole_q = (p.Hq & 3) == 0;
@@ -396,8 +440,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 6)
     };
     __syncwarp();                       // the previous token's table has been read
     if (own < pairs) {
-      const float2 c0 = turn_at(f0, pl.scale, pl.sign, pos), c1 = turn_at(f1, pl.scale, pl.sign, pos);
-      reinterpret_cast<float4*>(table)[g * rot + s] = make_float4(c0.x, c1.x, c0.y, c1.y);
+      const float2 c0 = turn_at<false>(f0, pl.scale, pl.sign, pos), c1 = turn_at<false>(f1, pl.scale, pl.sign, pos);
+      reinterpret_cast<float4*>(table)[g * kItemsOfHead + s] = make_float4(c0.x, c1.x, c0.y, c1.y);
     }
     __syncwarp();
     if (SCALAR) {
@@ -409,7 +453,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 6)
         const int xa = (HALF && j < pairs) ? j : 2 * j, xb = (HALF && j < pairs) ? j + pairs : 2 * j + 1;
         const E ea = src[xa], eb = src[xb];
         if (j < pairs && h < p.Hq + p.Hkv) {
-          const float* at = table + 4 * (((j & 7) >> 1) * rot + (j >> 3)) + (j & 1);
+          const float* at = table + 4 * (((j & 7) >> 1) * kItemsOfHead + (j >> 3)) + (j & 1);
           const float2 c = make_float2(at[0], at[2]);
           const float u = to_f32(ea), v = to_f32(eb);
           dst[xa] = __float2bfloat16_rn(fmaf(u, c.x, -(v * c.y)));
@@ -422,12 +466,12 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 6)
       continue;
     }
     Turn8 turn;
-    if (turns) turn.load(table, s, rot);
+    if (turns) turn.load(table, s);
     for (int h0 = 0;;) {
 #pragma unroll
       for (int k = 0; k < kAppendQ; ++k) {
         if (h0 + 4 * k < p.Hq) {
-          if (turns) rotate_item<HALF>(a[k], b[k], turn, 8 * s, pairs);
+          if (turns) rotate_item<HALF>(a[k], b[k], turn, s, pairs, kHeadDim);
           E* dst = qd + q_head(h0 + 4 * k) * kHeadDim;
           a[k].store(dst + ca);
           b[k].store(dst + cb);
@@ -439,7 +483,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 6)
     }
     if (row < 0) continue;
     for (int e = g; e < 2 * p.Hkv;) {
-      if (turns && e < p.Hkv) rotate_item<HALF>(ka, kb, turn, 8 * s, pairs);
+      if (turns && e < p.Hkv) rotate_item<HALF>(ka, kb, turn, s, pairs, kHeadDim);
       E* dst = kv_target(e);
       ka.store(dst + ca);
       kb.store(dst + cb);
@@ -450,29 +494,37 @@ __global__ void __launch_bounds__(32 * kAppendWarps, 6)
 }
 
 template <typename E>
-cudaError_t launch_rope_t(const la_rope_plan& plan, const RopeProblem& p, bool vec, cudaStream_t s) {
+cudaError_t launch_rope_t(const la_rope_plan& plan, const RopeProblem& p, bool vec, int sms, cudaStream_t s) {
   const Turns pl = turns_of(plan, p.inverse);
   const bool half = plan.layout == LA_ROPE_HALF;
   const int pairs = pl.pairs;
-  // Tokens per block: a full set of loads for every thread, at most 32 KB of cosines and sines, and
-  // (few tokens) no more than spreads them over two blocks per SM.
-  const int per_tok = p.heads * (vec ? p.head_dim / 16 : p.head_dim / 2);
-  long long tok = (long long)kRopeThreads * kItemsOf<E> / per_tok;
-  if (tok > 4096 / (pairs + 7)) tok = 4096 / (pairs + 7);
-  if (tok > p.tokens / 296) tok = p.tokens / 296;
+  if (vec) {
+    // One set of items for every thread: whole tokens, or a block of one token's heads.
+    const int ns = p.head_dim / 16, heads = kRopeThreads / ns * kItemsOf<E>;   // of a unit, over its tokens
+    const int hb = p.heads < heads ? p.heads : heads;
+    long long tok = heads / hb;
+    if (tok > p.tokens / (2 * sms)) tok = p.tokens / (2 * sms);   // few tokens: spread over the SMs
+    if (tok < 1) tok = 1;
+    const long long units = (p.tokens + tok - 1) / tok * ((p.heads + hb - 1) / hb);
+    const long long full = (long long)rope_ctas(half) * sms;
+    const dim3 grid((unsigned)(units < full ? units : full));
+    return launch_pdl(half ? rope_kernel<E, true> : rope_kernel<E, false>, grid, dim3(kRopeThreads), 0, s, pl, p,
+                      (int)tok, hb);
+  }
+  // Tokens per block: a few pairs for every thread, at most 32 KB of cosines and sines, and (few
+  // tokens) no more than spreads them over the SMs.
+  long long tok = 4LL * kRopeThreads / (p.heads * (p.head_dim / 2));
+  if (tok > 4096 / pairs) tok = 4096 / pairs;
+  if (tok > p.tokens / (2 * sms)) tok = p.tokens / (2 * sms);
   if (tok < 1) tok = 1;
   const dim3 grid((unsigned)((p.tokens + tok - 1) / tok));
-  const size_t smem = (size_t)tok * ((pairs + 7) / 8 * 8) * sizeof(float2);
-  if (vec)
-    return half ? launch_pdl(rope_kernel<E, true>, grid, dim3(kRopeThreads), smem, s, pl, p, (int)tok)
-                : launch_pdl(rope_kernel<E, false>, grid, dim3(kRopeThreads), smem, s, pl, p, (int)tok);
-  return half ? launch_pdl(rope_scalar_kernel<E, true>, grid, dim3(kRopeThreads), smem, s, pl, p, (int)tok)
-              : launch_pdl(rope_scalar_kernel<E, false>, grid, dim3(kRopeThreads), smem, s, pl, p, (int)tok);
+  return launch_pdl(half ? rope_scalar_kernel<E, true> : rope_scalar_kernel<E, false>, grid, dim3(kRopeThreads),
+                    (size_t)tok * pairs * sizeof(float2), s, pl, p, (int)tok);
 }
 
 }  // namespace
 
-cudaError_t launch_rope(const la_rope_plan& pl, const RopeProblem& p, int dtype, cudaStream_t s) {
+cudaError_t launch_rope(const la_rope_plan& pl, const RopeProblem& p, int dtype, int sms, cudaStream_t s) {
   const int es = dtype == LA_DTYPE_F32 ? 4 : 2;
   auto al = [&](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
   auto st = [&](long long n) { return n * es % 16 == 0; };
@@ -480,9 +532,9 @@ cudaError_t launch_rope(const la_rope_plan& pl, const RopeProblem& p, int dtype,
   const bool vec = p.head_dim % 16 == 0 && (pl.layout == LA_ROPE_INTERLEAVED || pl.rotary_dim % 16 == 0) &&
                    al(p.x) && al(p.out) && st(p.x_tok) && st(p.x_head) && st(p.y_tok) && st(p.y_head);
   switch (dtype) {
-    case LA_DTYPE_F32: return launch_rope_t<float>(pl, p, vec, s);
-    case LA_DTYPE_BF16: return launch_rope_t<__nv_bfloat16>(pl, p, vec, s);
-    case LA_DTYPE_F16: return launch_rope_t<__half>(pl, p, vec, s);
+    case LA_DTYPE_F32: return launch_rope_t<float>(pl, p, vec, sms, s);
+    case LA_DTYPE_BF16: return launch_rope_t<__nv_bfloat16>(pl, p, vec, sms, s);
+    case LA_DTYPE_F16: return launch_rope_t<__half>(pl, p, vec, sms, s);
   }
   return cudaErrorInvalidValue;
 }
@@ -490,7 +542,7 @@ cudaError_t launch_rope(const la_rope_plan& pl, const RopeProblem& p, int dtype,
 cudaError_t launch_rope_append(const la_rope_plan& plan, const RopeAppendProblem& p, int sms, cudaStream_t s) {
   // One warp per token while they fit on the GPU at once, else as many tokens in turn.
   const int tokens = p.B * p.T;
-  const int full = 6 * sms, blocks = (tokens + kAppendWarps - 1) / kAppendWarps;
+  const int full = kAppendCtas * sms, blocks = (tokens + kAppendWarps - 1) / kAppendWarps;
   const dim3 grid((unsigned)(blocks < full ? blocks : full)), block(32 * kAppendWarps);
   const Turns pl = turns_of(plan, false);
   const bool half = plan.layout == LA_ROPE_HALF;
