@@ -10,9 +10,12 @@
 // A key is a TMEM lane, so with the row statistics known each thread sums its own key's NQ
 // probabilities in registers: no maximum, no exchange between threads, one store per key.
 //
-// Bound: the second reading of K (256 bytes per key against 4 to read and 4 to write of the
-// weights), from L2 as far as the attention pass left it there. The exponentials (NQ per key, 16
-// per clock and SM) take a quarter of a tile's copy time at NQ = 48.
+// Bound: the second reading of K from HBM (256 bytes per key against 4 to read and 4 to write of the
+// weights): 8 sequences of 32768 keys add 27 us to the attention's 50 us, of which the copy is 20.5
+// us at the measured rate. The exponentials (NQ per key, 16 per clock and SM) take a quarter of a
+// tile's copy time at NQ = 48. Leaving a share of K in L2 for this reading (evict-last in the attention
+// kernel, 40 to 134 MB of K) measured slower at every share (79.0 us without, 80.4 to 85.9 us with):
+// the lines that stay push the streams and partials out.
 //
 // Plan: as the attention kernel's, without a fixed segment cost: every CTA gets the same
 // number of whole key tiles, +-1, whatever the mix of lengths.
@@ -244,19 +247,26 @@ __global__ void __launch_bounds__(kWThreads, 1)
     int* lim = reinterpret_cast<int*>(base + L.lim) + (warp - 2) * NQ;
     const uint32_t old_s = sb + (uint32_t)(L.old + group * kAhead * 512 + 4 * row);   // [kAhead][128]
     const float c2 = p.scale_log2;
-    pdl_wait();   // the merge (and so the attention) kernel is complete: lse2
+    // The group's first tile is gone through once before the merge kernel (and with it the attention) is
+    // complete, against statistics of +inf and to no effect: its instructions are then at hand when
+    // the statistics are (one image, all three kernels: 14.4 us without this, 13.5 us with it).
+    bool waited = false;
     int g = 0;
     bool ok = true;
     while (ok && it.next<true>(p, pre, blockIdx.x, sg)) {
       const long long head = (long long)sg.b * p.Hkv + sg.h;
-      __syncwarp();
-      for (int q = lane; q < NQ; q += 32) {
-        // A row that takes no part (operand padding, padding of a shorter window) adds 2^-inf.
-        const bool live = q < p.R && (!LIMITS || q < sg.w * p.G);
-        lse[q] = live ? __ldcg(kw.lse2 + head * p.rows_pad + q) : INFINITY;
-        if (LIMITS) lim[q] = live ? row_limit(p, sg.n, sg.w, q) : 0;
-      }
-      __syncwarp();
+      auto statistics = [&]() {
+        __syncwarp();
+#pragma unroll 1
+        for (int q = lane; q < NQ; q += 32) {
+          // A row that takes no part (operand padding, padding of a shorter window) adds 2^-inf.
+          const bool live = q < p.R && (!LIMITS || q < sg.w * p.G);
+          lse[q] = live && waited ? __ldcg(kw.lse2 + head * p.rows_pad + q) : INFINITY;
+          if (LIMITS) lim[q] = live ? row_limit(p, sg.n, sg.w, q) : 0;
+        }
+        __syncwarp();
+      };
+      statistics();
       // Window rows start afresh: their slots may hold the weight of an earlier occupant. The old
       // weights are copied to shared memory kAhead tiles ahead, each lane its own (a tile takes less
       // time than a read, and a register with a read in flight cannot be passed on).
@@ -275,7 +285,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
 #pragma unroll 1
       for (int i = 0; i < kAhead; ++i) read_ahead(sg.j0 + row + (skip + 2 * i) * kTileKeys, i);
 #pragma unroll 1
-      for (int t = skip, slot = 0; t < tiles; t += 2, slot = (slot + 1) % kAhead) {
+      for (int t = skip, slot = 0; t < tiles;) {
         const int jt = sg.j0 + t * kTileKeys, gt = g0 + t;
         const int key = jt + row, s = gt % kWSBufs;
         const bool key_ok = key < sg.j1;
@@ -297,7 +307,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
               sum[i & 3] += key < lim[c + i] ? fast_exp2(fmaf(x[i], c2, -lse[c + i])) : 0.f;
           }
           tc_fence_before();
-          mbar_arrive(bar(kWBarSEmpty + s));
+          if (waited) mbar_arrive(bar(kWBarSEmpty + s));
         } else {
 #pragma unroll
           for (int c = 0; c < NQ; c += kChunk) {
@@ -307,7 +317,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
             tc_wait_ld();
             if (c + kChunk >= NQ) {
               tc_fence_before();
-              mbar_arrive(bar(kWBarSEmpty + s));
+              if (waited) mbar_arrive(bar(kWBarSEmpty + s));
             }
 #pragma unroll
             for (int e = 0; e < kChunk && c + e < NQ; e += 4) {
@@ -322,10 +332,19 @@ __global__ void __launch_bounds__(kWThreads, 1)
         float old;
         asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
         asm volatile("ld.shared.f32 %0, [%1];" : "=f"(old) : "r"(old_s + (uint32_t)slot * 512u) : "memory");
-        if (key_ok) kw.out[head * p.S + key] = fmaf(kw.decay, old, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+        if (key_ok && waited) kw.out[head * p.S + key] = fmaf(kw.decay, old, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+        if (!waited) {
+          pdl_wait();
+          waited = true;
+          statistics();
+          continue;
+        }
         read_ahead(key + 2 * kAhead * kTileKeys, slot);
+        t += 2;
+        slot = (slot + 1) % kAhead;
       }
     }
+    if (!waited) pdl_wait();   // (the kernel must not complete before its predecessors)
     asm volatile("cp.async.wait_all;" ::: "memory");
   }
 
