@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) evict_move_kernel(Evi
 int evict_ctas(int S, int heads) {
   // One CTA up to 8192 keys of capacity (16 a thread), then one per 4096, at most a portable cluster,
   // and no more than are resident together: a CTA takes an SM, and clusters of 8 leave up to a
-  // quarter of the SMs out (16 heads of 32768 keys: 8 CTAs each 28 us in two waves, 4 each 16 us).
+  // quarter of the SMs out (16 heads of 32768 keys: 8 CTAs each 28 us in two waves, 4 each 18 us).
   if (S <= 2 * kSelTile) return 1;
   int c = 2;
   while (c < kMaxEvictCtas && c * kSelTile < S && 2 * c * heads <= 112) c *= 2;

@@ -12,13 +12,12 @@
 // product, its reduction and the conversions took a third of the kernel's instructions). Its upper
 // 32 bits become half turns in [-1, 1), of which sine and cosine are taken in 32 bits: with full
 // accuracy for fp32 results, and for 16-bit ones, whose rounding is 2^-12 of the value at best, with the
-// fast functions (2^-21 absolute). A block computes the
-// cosines and sines of its tokens once into shared memory; every head of those tokens uses
-// them, so the transcendental work is 1/(heads) of the elements.
+// fast functions (2^-21 absolute).
 //
-// Bound: memory. One item is 32 bytes of input (two 16-byte chunks, the two halves of 8 pairs in
-// the half layout) and 32 bytes of output, and a thread's loads are issued before the angles are
-// computed, so that the two overlap.
+// Bound: memory. An item is 16-byte chunks holding both channels of 8 pairs (4 in fp32). In la_rope a
+// thread keeps its pairs over all its tokens and heads, so a token's cosines are taken once for the
+// heads that the thread turns; in la_rope_append a warp owns a token and shares its cosines over all
+// heads through a table of its own in shared memory.
 #include <cmath>
 
 #include "pbd_common.cuh"
@@ -480,6 +479,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
       h0 += 4 * kAppendQ;
       if (h0 >= p.Hq) break;
       load_q(h0);
+      if (!whole_q) __syncwarp();       // in place, a repeated head is read by every lane before one writes it
     }
     if (row < 0) continue;
     for (int e = g; e < 2 * p.Hkv;) {

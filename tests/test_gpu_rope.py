@@ -229,6 +229,28 @@ def test_append_prompt_defaults():
     assert torch.equal(k[:, :, :T], want_k.transpose(1, 2)) and torch.equal(v[:, :, :T], vn.transpose(1, 2))
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 1), (6, 2), (18, 2), (22, 11), (35, 5)])
+@pytest.mark.parametrize("layout,rotary", [("half", 128), ("half", 64), ("half", 50), ("interleaved", 128),
+                                           ("interleaved", 48)])
+def test_append_in_place_of_any_heads(Hq, Hkv, layout, rotary):
+    """Head counts that do not divide over a warp, q in place: the bits of a separate output."""
+    B, T, S = 3, 130, 192
+    rows = [130, 0, 77]
+    q, kn, vn, k, v, _ = _append_case(B, T, S, None, rows, 0, False, Hq=Hq, Hkv=Hkv, seed=Hq)
+    cfg, plan = bmw.Config.make(B, Hq, Hkv, S), bmw.RopePlan.make(rotary, layout=layout)
+    n = torch.tensor(rows, dtype=torch.int32, device="cuda")
+    x, apart, k2, v2 = q.clone(), q.clone(), k.clone(), v.clone()
+    bmw.la_rope_append(cfg, plan, q, kn, vn, None, apart, k, v, row_lens=n)
+    bmw.la_rope_append(cfg, plan, q, kn, vn, None, q, k2, v2, row_lens=n)
+    assert torch.equal(k, k2) and torch.equal(v, v2)
+    for b, r in enumerate(rows):
+        assert torch.equal(q[b, :r], apart[b, :r])
+        assert torch.isnan(q[b, r:]).all()
+        ref = oracle.rotate(x[b, :r], np.arange(r), oracle.rope_angles(rotary), layout)
+        if r:
+            assert_turned(apart[b, :r], x[b, :r], ref, rotary, layout)
+
+
 def test_append_skips_pages_outside_the_pool():
     B, T, page = 1, 6, 64
     q, kn, vn, k, v, table = _append_case(B, T, 128, [60], [6], page, False)
