@@ -232,13 +232,18 @@ __device__ __forceinline__ void window_load_append(const Problem& p, const Segme
   const int P = sg.n - sg.w;
   const int cnt = (w1 - w0) * 16;
 #pragma unroll
+  for (int u = 0; u < kWinRegs; ++u) {     // (all loads in flight together)
+    const int idx = lane + 32 * u;
+    const int w = w0 + (idx >> 4), ch = idx & 15;
+    if (idx < cnt)
+      v[u] = load_row16(reinterpret_cast<const uint4*>(
+                            src + (((size_t)sg.b * p.W + w) * p.Hkv + sg.h) * kHeadDim) + ch);
+  }
+#pragma unroll
   for (int u = 0; u < kWinRegs; ++u) {
     const int idx = lane + 32 * u;
     if (idx < cnt) {
       const int w = w0 + (idx >> 4), ch = idx & 15;
-      const uint4* s = reinterpret_cast<const uint4*>(
-          src + (((size_t)sg.b * p.W + w) * p.Hkv + sg.h) * kHeadDim) + ch;
-      v[u] = __ldg(s);
       uint4* d = reinterpret_cast<uint4*>(
           cache + (size_t)kv_row<PAGED>(p, sg.b, sg.h, P + w) * kHeadDim) + ch;
       *d = v[u];

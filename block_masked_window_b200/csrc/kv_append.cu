@@ -22,8 +22,8 @@ __global__ void __launch_bounds__(256) kv_append_kernel(
   const int h = (int)(row % Hkv);
   const int w = (int)((row / Hkv) % W);
   const int b = (int)(row / ((long long)Hkv * W));
-  const int P = __ldg(seq_lens + b);
-  const int wb = window_lens ? __ldg(window_lens + b) : W;   // this sequence's window
+  const int P = load_len(seq_lens + b);
+  const int wb = window_lens ? load_len(window_lens + b) : W;   // this sequence's window
   if (P < 0 || wb < 1 || wb > W || (long long)P + wb > S) return;  // flagged by the attention kernels
   if (w >= wb) return;                         // padding row of a shorter window
   constexpr int kVec = kHeadDim * 2 / 16;      // 16 vectors of 16 bytes per row
@@ -31,9 +31,9 @@ __global__ void __launch_bounds__(256) kv_append_kernel(
   const size_t src = (size_t)row * kVec + c;   // [B, W, Hkv, D] row-major
   const size_t dst = (((size_t)b * Hkv + h) * S + (size_t)(P + w)) * kVec + c;
   if (lane < kVec) {
-    k_cache[dst] = __ldg(k_new + src);
+    k_cache[dst] = load_row16(k_new + src);
   } else {
-    v_cache[dst] = __ldg(v_new + src);
+    v_cache[dst] = load_row16(v_new + src);
   }
 }
 

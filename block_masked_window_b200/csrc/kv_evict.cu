@@ -99,11 +99,11 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictProbl
   }
   pdl_trigger();
   pdl_wait();
-  const int P = __ldg(p.seq_lens + b);
+  const int P = load_len(p.seq_lens + b);
   const bool valid = P >= 0 && P <= p.S;
   const int n = valid ? P : 0;
   const int Lk = min(n, p.budget);
-  const long long next = p.next_pos ? (long long)__ldg(p.next_pos + b) : (long long)n;
+  const long long next = p.next_pos ? (long long)load_len(p.next_pos + b) : (long long)n;
   const float* w = p.weights + (size_t)bh * p.S;
   const int* pos = p.key_pos ? p.key_pos + (size_t)bh * p.S : nullptr;
   int* holes = p.slots + ((size_t)bh * C + rank) * 2 * p.part;

@@ -109,16 +109,30 @@ __device__ inline float* slot_ptr(const Problem& p, int slot) {
 
 // Loads of seq_lens / window_lens. kL2 = true reads through L2 only (ld.global.cg): the only
 // form used before a kernel's dependency wait, so that no L1 line of a value the previous
-// kernel may still write can be hit after the wait. (Host-callable for the plan inspection
-// entry point, where the arrays are host memory.)
+// kernel may still write can be hit after the wait. Otherwise a plain coherent load, for use after the
+// wait: the previous kernel may write the lengths while this one has already started, which rules
+// out the read-only path. (Host-callable for the plan inspection entry point, where the arrays
+// are host memory.)
 template <bool kL2 = false>
 __host__ __device__ inline int load_len(const int32_t* a) {
 #ifdef __CUDA_ARCH__
-  return kL2 ? __ldcg(a) : __ldg(a);
+  if (kL2) return __ldcg(a);
+  int v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(a));
+  return v;
 #else
   return *a;
 #endif
 }
+
+#ifdef __CUDACC__
+// 16 bytes of data that the previous kernel may have written while this one was starting.
+__device__ __forceinline__ uint4 load_row16(const uint4* a) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(a));
+  return v;
+}
+#endif
 
 // Window length of sequence b (W when all sequences share it).
 template <bool kL2 = false>

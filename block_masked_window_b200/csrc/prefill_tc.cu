@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(256) prefill_v16_kernel(PrefillProblem p) {
   const int t = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
   pdl_wait();   // V and seq_lens may come from the previous kernel of the stream
   pdl_trigger();
-  int Tb = __ldg(p.seq_lens + b);
+  int Tb = load_len(p.seq_lens + b);
   if (Tb < 0 || Tb > p.T || Tb > p.S) Tb = 0;   // (the attention kernel flags it)
   const int r0 = t * kBN;
   const int rows = max(0, min(kBN, Tb - r0));
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(256) prefill_v16_kernel(PrefillProblem p) {
   uint4* dst = reinterpret_cast<uint4*>(p.v16 + ((size_t)(b * p.Hkv + hk) * p.Tp + r0) * kHeadDim);
   float vmax = 0.f;
   for (int c = threadIdx.x; c < rows * (kHeadDim / 8); c += blockDim.x) {
-    const uint4 x = __ldg(src + c);   // 8 bf16
+    const uint4 x = load_row16(src + c);   // 8 bf16
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     uint32_t o[4];
 #pragma unroll
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   pdl_wait();
 
   // Tokens of this sequence; an invalid length gives zero rows and the sticky flag.
-  int Tb = __ldg(p.seq_lens + b);
+  int Tb = load_len(p.seq_lens + b);
   if (Tb < 0 || Tb > p.T || Tb > p.S) {
     if (tid == 0 && h == 0 && tile == ntiles - 1) atomicOr(&p.hdr->err, kErrSeqOverflow);
     Tb = 0;

@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(HALF))
       if (at[k] < nt && h0 + head[k] < p.heads) {
         a[k].load(x + from[k]);
         b[k].load(x + from[k] + gap);
-        pos[k] = __ldg(p.positions + t0 + at[k]);
+        pos[k] = load_len(p.positions + t0 + at[k]);
       }
     }
 #pragma unroll
@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kRopeThreads)
   const int nt = (int)min((long long)tok, p.tokens - t0);
   for (int i = threadIdx.x; i < nt * pairs; i += kRopeThreads) {
     const int t = i / pairs;
-    s_cs[i] = turn_at<true>(pl.f[i - t * pairs], pl.scale, pl.sign, __ldg(p.positions + t0 + t));
+    s_cs[i] = turn_at<true>(pl.f[i - t * pairs], pl.scale, pl.sign, load_len(p.positions + t0 + t));
   }
   __syncthreads();
   const int half = p.head_dim >> 1;
@@ -415,9 +415,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
       load_kv(g);
     }
     const int sq = tok / p.T, i = tok - sq * p.T;
-    const int P = p.seq_lens ? __ldg(p.seq_lens + sq) : 0;
-    const int w = p.row_lens ? __ldg(p.row_lens + sq) : p.T;
-    const long long pos = (long long)(p.pos0 ? __ldg(p.pos0 + sq) : P) + i;
+    const int P = p.seq_lens ? load_len(p.seq_lens + sq) : 0;
+    const int w = p.row_lens ? load_len(p.row_lens + sq) : p.T;
+    const long long pos = (long long)(p.pos0 ? load_len(p.pos0 + sq) : P) + i;
     // Padding, or a sequence whose lengths are invalid: nothing is written.
     if (P < 0 || w < 0 || w > p.T || (long long)P + w > p.S || i >= w) continue;
     const int slot = P + i;

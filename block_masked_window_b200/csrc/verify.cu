@@ -87,10 +87,10 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyProblem a) {
   const E* q = a.q ? static_cast<const E*>(a.q) + (long long)b * a.q_batch : nullptr;
   const int* drafts = a.drafts + (long long)b * a.K;
   if (warp == 0) {
-    const int len = a.draft_lens ? __ldg(a.draft_lens + b) : a.K;
+    const int len = a.draft_lens ? load_len(a.draft_lens + b) : a.K;
     bool ok = false;
     if (lane < a.K && lane < len) {
-      const int x = __ldg(drafts + lane);
+      const int x = load_len(drafts + lane);
       if (x >= 0 && x < a.V) {             // a token outside the vocabulary has probability 0
         const double px = to_f64(p[(long long)lane * a.p_row + x]);
         const double qx = q ? to_f64(q[(long long)lane * a.q_row + x]) : 1.0;
@@ -111,10 +111,10 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyProblem a) {
   int* tokens = a.tokens + (long long)b * (a.K + 1);
   if (rank == 0) {
     for (int i = tid; i <= a.K; i += kVThreads)
-      if (!valid || i != n) tokens[i] = valid && i < n ? __ldg(drafts + i) : -1;
+      if (!valid || i != n) tokens[i] = valid && i < n ? load_len(drafts + i) : -1;
     if (tid == 0) {
       a.accepted[b] = valid ? n : -1;
-      if (a.seq_lens_out) a.seq_lens_out[b] = a.seq_lens[b] + (valid ? n + 1 : 0);
+      if (a.seq_lens_out) a.seq_lens_out[b] = load_len(a.seq_lens + b) + (valid ? n + 1 : 0);
     }
   }
   if (!valid) return;                      // (the whole cluster)
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyProblem a) {
   const E* pr = p + (long long)n * a.p_row;
   const bool rejected = n < len;
   const E* qr = rejected && q ? q + (long long)n * a.q_row : nullptr;
-  const int skip = rejected && !q ? __ldg(drafts + n) : -1;
+  const int skip = rejected && !q ? load_len(drafts + n) : -1;
   const int per = ((a.V + C * kVWarps - 1) / (C * kVWarps) + 31) & ~31;   // entries of a range
   const double v = (double)__ldg(a.sample_u + b);
   // First the residual, where a draft was rejected; then, if that is empty, p itself.

@@ -201,3 +201,66 @@ def test_decode_loop(page, graphed):
             assert_parity(o.cpu(), ref, f"step {step}")
     assert bmw.la_pbd_check(L.ws) == 0 and bmw.la_pbd_check(L.ews) == 0
     assert max(pos) > budget + W
+
+
+@pytest.mark.parametrize("attention", ["weights", "attn", "varwin", "step"])
+def test_lengths_from_the_kernel_before(attention):
+    """Lengths that one kernel writes are read by the next, which may have started before that write:
+    a chain of steps in a graph gives the bits of the same calls one at a time."""
+    B, S, V, steps, hq = 96, 512, 16, 24, 16
+    g = torch.Generator().manual_seed(11)
+    r = lambda *n: torch.randn(n, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    i32 = lambda *n, v=0: torch.full(n, v, dtype=torch.int32, device="cuda")  # noqa: E731
+    q, kn, vn = r(B, W, hq, 128), r(B, W, HKV, 128), r(B, W, HKV, 128)
+    k0, v0 = r(B, HKV, S, 128), r(B, HKV, S, 128)
+    p = torch.softmax(torch.randn(B, W, V, generator=g), -1).cuda()
+    drafts = torch.randint(V, (steps, B, W - 1), generator=g, dtype=torch.int32).cuda()
+    u = (torch.rand(steps, B, W - 1, generator=g) * 0.15).cuda()
+    su = torch.rand(steps, B, generator=g).cuda()
+    first = torch.randint(0, S - steps * W - W, (B,), generator=g, dtype=torch.int32).cuda()
+    wl = i32(B, v=W)
+    pos0 = torch.arange(steps, dtype=torch.int32, device="cuda").mul(1000).unsqueeze(1).repeat(1, B)
+    cfg, plan = bmw.Config.make(B, hq, HKV, S), bmw.RopePlan.make(128)
+    ws, ews = bmw.WeightsWorkspace(cfg, W), bmw.EvictWorkspace(cfg)
+    k, v, lens, key_pos = k0.clone(), v0.clone(), first.clone(), i32(B, HKV, S, v=-1)
+    weights = torch.zeros(B, HKV, S, device="cuda")
+    out = torch.zeros(steps, B, W, hq, 128, dtype=torch.bfloat16, device="cuda")
+    q_rot, tokens, acc = torch.empty_like(q), i32(steps, B, W), i32(steps, B)
+
+    def chain(after):
+        k.copy_(k0), v.copy_(v0), lens.copy_(first), key_pos.fill_(-1), weights.zero_()
+        after()
+        for t in range(steps):
+            bmw.la_rope_append(cfg, plan, q, kn, vn, lens, q_rot, k, v, pos0=pos0[t], key_pos=key_pos)
+            after()
+            if attention == "weights":
+                bmw.la_pbd_attn_weights(cfg, q_rot, k, v, lens, W, out[t], weights, ws, weights_in=weights)
+            elif attention == "attn":
+                bmw.la_pbd_attn(cfg, q_rot, k, v, lens, W, out[t], ws)
+            elif attention == "varwin":
+                bmw.la_pbd_attn_varwin(cfg, q_rot, k, v, lens, wl, W, out[t], ws)
+            else:
+                bmw.la_pbd_step(cfg, q_rot, kn, vn, k, v, lens, W, out[t], ws)
+            after()
+            bmw.la_pbd_verify(p, None, drafts[t], u[t], su[t], tokens[t], acc[t], seq_lens=lens, seq_lens_out=lens)
+            after()
+            if attention == "attn":        # straight from the new lengths to the attention
+                bmw.la_pbd_attn(cfg, q_rot, k, v, lens, W, out[t], ws)
+                after()
+            if t % 8 == 7:
+                bmw.la_kv_evict(cfg, weights, lens, S // 2, k, v, weights, lens, ews, key_pos=key_pos,
+                                key_pos_out=key_pos)
+                after()
+        return [x.clone() for x in (k, v, lens, key_pos, weights, out, tokens, acc)]
+
+    want = chain(torch.cuda.synchronize)
+    assert int(want[-1].max()) > int(want[-1].min())       # the sequences advance differently
+    assert int(want[2].max()) + W <= S
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain(lambda: None)
+    for _ in range(10):
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
