@@ -590,6 +590,7 @@ def _ext():
     global _EXT
     if _EXT is None:
         load()
+        import torch  # noqa: F401  (the module links torch's libraries)
         try:
             from . import _la_torch
         except ImportError as e:

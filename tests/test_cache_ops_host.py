@@ -2,6 +2,9 @@
 formulas, the oracle's own properties, and every refusal that needs no device."""
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -270,3 +273,10 @@ def test_oracle_verification_distribution():
     np.testing.assert_allclose(counts, p[0], atol=0.02)
     # a miss and an empty residual: the target row itself
     assert oracle.verify(p[:, :], np.array([[1.0, 1.0, 1.0, 1.0]]), [3], [0.5], 0.6) == ([1], 0)
+
+
+def test_binding_loads_by_itself(lib):
+    """The module over torch tensors is loaded in a process that has not imported torch."""
+    code = ("import sys, block_masked_window_b200 as bmw; assert 'torch' not in sys.modules; "
+            "assert hasattr(bmw._ext(), 'rope')")
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=os.path.dirname(os.path.dirname(__file__)))
