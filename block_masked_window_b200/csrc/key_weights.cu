@@ -282,6 +282,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
       const int skip = (g ^ group) & 1, tiles = (sg.j1 - sg.j0 + kTileKeys - 1) / kTileKeys;
       const int g0 = g;
       g += tiles;
+      // The copies that ran past the segment before (zeros) use the same slots, and a thread's copies land in
+      // no order of their own: they are complete before the first ones of this segment.
+      asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1
       for (int i = 0; i < kAhead; ++i) read_ahead(sg.j0 + row + (skip + 2 * i) * kTileKeys, i);
 #pragma unroll 1

@@ -141,6 +141,16 @@ def test_accumulates_in_place():
     _run([70, 900], 6, decay=0.97, alias=True)
 
 
+@pytest.mark.parametrize("page", [0, 64])
+def test_old_weights_over_many_segments(page):
+    """Several short sequences to a CTA: the copies of old weights that run past one sequence's keys and
+    the first ones of the next use the same slots of shared memory. Every old weight arrives."""
+    lens = torch.randint(0, 700, (160,), generator=torch.Generator().manual_seed(5)).tolist()
+    wl = [1 + i % 6 for i in range(160)]
+    for seed in range(3):
+        _run(lens, 6, wl=wl if seed == 2 else None, page=page, decay=0.75, seed=seed, alias=seed == 1)
+
+
 def test_sharp_rows():
     """Scores of hundreds: all the weight on single keys, the rest vanish without a NaN."""
     _run([300, 2000], 6, gain=40.0)
