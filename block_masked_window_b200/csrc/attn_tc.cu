@@ -174,7 +174,7 @@ __device__ __forceinline__ void store_pt16_impl(uint32_t prow, int c, const floa
 template <bool PAGED>
 __device__ __forceinline__ int kv_row(const Problem& p, int b, int h, int j) {
   if (!PAGED) return (b * p.Hkv + h) * p.S + j;
-  const int page = __ldg(p.block_table + (size_t)b * p.pages_per_seq + j / p.page_size);
+  const int page = load_len(p.block_table + (size_t)b * p.pages_per_seq + j / p.page_size);
   return (page * p.Hkv + h) * p.page_size + (j % p.page_size);
 }
 

@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) evict_move_kernel(Evi
   auto row = [&](int bh, int slot) -> long long {   // -1: the table names no page of the pool
     if (!p.block_table) return ((long long)bh * p.S + slot) * (kHeadDim / 8);
     const int b = bh / p.Hkv, h = bh - b * p.Hkv;
-    const int page = __ldg(p.block_table + (size_t)b * p.pages_per_seq + slot / p.page_size);
+    const int page = load_len(p.block_table + (size_t)b * p.pages_per_seq + slot / p.page_size);
     if (page < 0 || page >= p.num_pages) return -1;
     return (((long long)page * p.Hkv + h) * p.page_size + slot % p.page_size) * (kHeadDim / 8);
   };

@@ -107,11 +107,11 @@ __device__ inline float* slot_ptr(const Problem& p, int slot) {
   return p.partials + (size_t)slot * slot_floats(p.rows_pad);
 }
 
-// Loads of seq_lens / window_lens. kL2 = true reads through L2 only (ld.global.cg): the only
-// form used before a kernel's dependency wait, so that no L1 line of a value the previous
-// kernel may still write can be hit after the wait. Otherwise a plain coherent load, for use after the
-// wait: the previous kernel may write the lengths while this one has already started, which rules
-// out the read-only path. (Host-callable for the plan inspection entry point, where the arrays
+// Loads of seq_lens / window_lens, and of page table entries. kL2 = true reads through L2 only
+// (ld.global.cg): the only form used before a kernel's dependency wait, so that no L1 line of a value
+// the previous kernel may still write can be hit after the wait. Otherwise a plain coherent load, for
+// use after the wait: the previous kernel may write these while this one has already started, which
+// rules out the read-only path. (Host-callable for the plan inspection entry point, where the arrays
 // are host memory.)
 template <bool kL2 = false>
 __host__ __device__ inline int load_len(const int32_t* a) {
@@ -126,7 +126,12 @@ __host__ __device__ inline int load_len(const int32_t* a) {
 }
 
 #ifdef __CUDACC__
-// 16 bytes of data that the previous kernel may have written while this one was starting.
+// The same for a float, and for 16 bytes of data.
+__device__ __forceinline__ float load_f32(const float* a) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(a));
+  return v;
+}
 __device__ __forceinline__ uint4 load_row16(const uint4* a) {
   uint4 v;
   asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(a));

@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps, kAppendCtas)
     const int slot = P + i;
     long long row, head_rows;           // cache row of KV head 0 (-1: none), rows between heads
     if (p.block_table) {
-      const int page = __ldg(p.block_table + (size_t)sq * p.pages_per_seq + slot / p.page_size);
+      const int page = load_len(p.block_table + (size_t)sq * p.pages_per_seq + slot / p.page_size);
       row = page >= 0 && page < p.num_pages ? (long long)page * p.Hkv * p.page_size + slot % p.page_size : -1;
       head_rows = p.page_size;
     } else {

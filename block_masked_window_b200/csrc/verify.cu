@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyProblem a) {
       if (x >= 0 && x < a.V) {             // a token outside the vocabulary has probability 0
         const double px = to_f64(p[(long long)lane * a.p_row + x]);
         const double qx = q ? to_f64(q[(long long)lane * a.q_row + x]) : 1.0;
-        ok = (double)__ldg(a.u + (long long)b * a.K + lane) * qx < px;
+        ok = (double)load_f32(a.u + (long long)b * a.K + lane) * qx < px;
       }
     }
     const uint32_t miss = ~__ballot_sync(0xffffffffu, ok);
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyProblem a) {
   const E* qr = rejected && q ? q + (long long)n * a.q_row : nullptr;
   const int skip = rejected && !q ? load_len(drafts + n) : -1;
   const int per = ((a.V + C * kVWarps - 1) / (C * kVWarps) + 31) & ~31;   // entries of a range
-  const double v = (double)__ldg(a.sample_u + b);
+  const double v = (double)load_f32(a.sample_u + b);
   // First the residual, where a draft was rejected; then, if that is empty, p itself.
   bool rest = rejected;
   auto entry = [&](int j, E x, E less) {
