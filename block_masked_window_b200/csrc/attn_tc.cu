@@ -223,7 +223,9 @@ __device__ __forceinline__ bool tile_window(const Problem& p, const Segment& sg,
   return lo < hi;
 }
 
-// Lane l holds chunks l, l + 32, ... of the rows [w0, w1) (16 chunks of 16 bytes per row).
+// Lane l holds chunks l, l + 32, ... of the rows [w0, w1) (16 chunks of 16 bytes per row; w0 < w1). All
+// loads are in flight before the first store, and those past the rows read the last row again: with a
+// predicate on each every small step was slower, appending or not (tiny step 9.9 us, 9.6 without).
 template <bool PAGED>
 __device__ __forceinline__ void window_load_append(const Problem& p, const Segment& sg,
                                                    const __nv_bfloat16* src,
@@ -232,12 +234,10 @@ __device__ __forceinline__ void window_load_append(const Problem& p, const Segme
   const int P = sg.n - sg.w;
   const int cnt = (w1 - w0) * 16;
 #pragma unroll
-  for (int u = 0; u < kWinRegs; ++u) {     // (all loads in flight together)
-    const int idx = lane + 32 * u;
-    const int w = w0 + (idx >> 4), ch = idx & 15;
-    if (idx < cnt)
-      v[u] = load_row16(reinterpret_cast<const uint4*>(
-                            src + (((size_t)sg.b * p.W + w) * p.Hkv + sg.h) * kHeadDim) + ch);
+  for (int u = 0; u < kWinRegs; ++u) {
+    const int w = min(w0 + ((lane + 32 * u) >> 4), w1 - 1);
+    v[u] = load_row16(reinterpret_cast<const uint4*>(
+                          src + (((size_t)sg.b * p.W + w) * p.Hkv + sg.h) * kHeadDim) + (lane & 15));
   }
 #pragma unroll
   for (int u = 0; u < kWinRegs; ++u) {

@@ -23,7 +23,8 @@ constexpr int kCombineMaxSlots = 1024;   // >= partials of one sequence (<= grid
 // kMerge partials are loaded in the first round trip; with kMerge = 4 the kernel needs so few
 // registers that 12 blocks fit on an SM, so a batch of many short split sequences (thousands
 // of rows, two or three partials each) is merged in one wave of blocks.
-template <int kMerge>
+// kStats: the rows' statistics are written for the key weights (max context 10.6 -> 10.5 us without them).
+template <int kMerge, bool kStats>
 __global__ void __launch_bounds__(32 * kCombineRows, kMerge <= 4 ? 12 : 1) pbd_combine_kernel(Problem p) {
   __shared__ float s_w[kCombineRows][kCombineMaxSlots];   // (16 KB)
   pdl_trigger();
@@ -152,13 +153,19 @@ __global__ void __launch_bounds__(32 * kCombineRows, kMerge <= 4 ? 12 : 1) pbd_c
     acc.w = fmaf(w, v.w, acc.w);
   }
   const float inv = 1.f / L;
-  if (p.lse2 && lane == 0) p.lse2[(size_t)s * p.rows_pad + r] = M + log2f(L);
+  if (kStats && lane == 0) p.lse2[(size_t)s * p.rows_pad + r] = M + log2f(L);
   __nv_bfloat162 o01 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
   __nv_bfloat162 o23 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
   uint2 packed;
   packed.x = *reinterpret_cast<uint32_t*>(&o01);
   packed.y = *reinterpret_cast<uint32_t*>(&o23);
   reinterpret_cast<uint2*>(dst)[lane] = packed;
+}
+
+template <int kMerge>
+static cudaError_t launch_combine_n(const Problem& p, dim3 grid, cudaStream_t stream) {
+  return launch_pdl(p.lse2 ? pbd_combine_kernel<kMerge, true> : pbd_combine_kernel<kMerge, false>, grid,
+                    dim3(32 * kCombineRows), 0, stream, p);
 }
 
 cudaError_t launch_combine(const Problem& p, cudaStream_t stream) {
@@ -170,12 +177,12 @@ cudaError_t launch_combine(const Problem& p, cudaStream_t stream) {
   const long long tiles = (p.S + p.unit - 1) / p.unit;
   const long long pieces = tiles < p.num_ctas ? tiles : p.num_ctas;
   if (pieces > 16 && (long long)p.B * p.Hkv <= 4)
-    return launch_pdl(pbd_combine_kernel<40>, grid, dim3(32 * kCombineRows), 0, stream, p);
+    return launch_combine_n<40>(p, grid, stream);
   // With at least half as many (sequence, KV head) pairs as attention CTAs, a pair spans few
   // CTAs (a longer one still merges correctly, through the loop past the first batch).
   if (2LL * p.B * p.Hkv >= p.num_ctas)
-    return launch_pdl(pbd_combine_kernel<4>, grid, dim3(32 * kCombineRows), 0, stream, p);
-  return launch_pdl(pbd_combine_kernel<16>, grid, dim3(32 * kCombineRows), 0, stream, p);
+    return launch_combine_n<4>(p, grid, stream);
+  return launch_combine_n<16>(p, grid, stream);
 }
 
 }  // namespace la

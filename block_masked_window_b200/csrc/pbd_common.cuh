@@ -58,10 +58,6 @@ struct Problem {
   float* partials;              // slots, see slot_floats
   WsHeader* hdr;
   int* pre_g;                   // [B+1] prefix sums of plan units, written by attention CTA 0
-  // Row statistics for the key weights (null: not wanted): log2 of each row's sum of
-  // exponentials, [B * Hkv, rows_pad]. Written by whichever kernel finishes the row: the attention
-  // kernel for a sequence it holds whole, else the merge. Rows without keys are not written.
-  float* lse2;
   int B, Hq, Hkv, G, W, S;      // G = Hq / Hkv; W = the (longest) window length
   int R;                        // rows per sequence = W * G
   int rows_pad;                 // R rounded up to 16: rows per partial slot
@@ -74,6 +70,11 @@ struct Problem {
   long long wait_limit_ns;      // limit of every bounded device-side wait (tcgen05 kernel)
   int stall_test;               // self-tests: 1 = the first S^T completion is never signalled,
                                 //             2 = the plan made before the wait is rejected
+  // Row statistics for the key weights (null: not wanted): log2 of each row's sum of
+  // exponentials, [B * Hkv, rows_pad]. Written by whichever kernel finishes the row: the attention
+  // kernel for a sequence it holds whole, else the merge. Rows without keys are not written. (Last:
+  // what every call reads keeps its place in the parameters.)
+  float* lse2;
 };
 
 // Launch parameters of the block-causal prefill kernel.
