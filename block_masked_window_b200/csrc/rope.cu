@@ -9,10 +9,10 @@
 //
 // Angles: f_i is handed to the kernels as a 64-bit fraction of a turn, so that t f_i modulo a turn is
 // one wrapping integer product (error below 2^-33 turns at t = 2^31; in 64-bit floating point the
-// product, its reduction and the conversions took a third of the kernel's instructions). Its upper
-// 32 bits become half turns in [-1, 1), of which sine and cosine are taken in 32 bits: with full
-// accuracy for fp32 results, and for 16-bit ones, whose rounding is 2^-12 of the value at best, with the
-// fast functions (2^-21 absolute).
+// product, its reduction and the conversions took a third of the kernel's instructions). Sine and cosine
+// are taken of it in 32 bits: for fp32 results of what is left of it after whole quarter turns, with an
+// error near a rounding's, and for 16-bit ones, whose rounding is 2^-12 of the value at best, of its
+// upper 32 bits with the fast functions (2^-21 absolute).
 //
 // Bound: memory. An item is 16-byte chunks holding both channels of 8 pairs (4 in fp32). In la_rope a
 // thread keeps its pairs over all its tokens and heads, so a token's cosines are taken once for the
@@ -119,13 +119,40 @@ Turns turns_of(const la_rope_plan& pl, bool inverse) {
   return t;
 }
 
+// Sine and cosine of x half turns, |x| <= 1/4 and a little: the Taylor series in x to degrees 9 and 10
+// (cut off below 2^-28), with pi in two parts because its first factor stands alone in the sine. Errors
+// against exact values over all x: sine 1.4e-8 rms, cosine 1.9e-8, where a correct rounding has 1.1e-8 and
+// 1.7e-8. (sincospif reduces its argument first, which has been done here: 37.3 us for 12291 x 16 x 128
+// fp32 with it, 33.1 so.)
+__device__ __forceinline__ void sincos_quarter(float x, float* s, float* c) {
+  const float z = x * x;
+  float p = fmaf(z, 0.0821458866f, -0.599264529f);   // pi^9 / 9!, -pi^7 / 7!, pi^5 / 5!, -pi^3 / 3!
+  p = fmaf(z, p, 2.55016404f);
+  p = fmaf(z, p, -5.16771278f);
+  p = fmaf(z, p, -8.74227766e-8f);                   // pi less its fp32 value
+  *s = fmaf(x, 3.14159274f, x * p);
+  float q = fmaf(z, -0.0258068914f, 0.235330631f);   // -pi^10 / 10!, pi^8 / 8!, -pi^6 / 6!, pi^4 / 4!
+  q = fmaf(z, q, -1.33526277f);
+  q = fmaf(z, q, 4.05871213f);
+  q = fmaf(z, q, -4.93480220f);                      // -pi^2 / 2!
+  *c = fmaf(z, q, 1.f);
+}
+
 // (scaled cosine, scaled sine) at position t of a pair that turns by the fraction f per position.
 template <bool EXACT>
 __device__ __forceinline__ float2 turn_at(unsigned long long f, float scale, float sign, long long t) {
   const int half = (int)((f * (unsigned long long)t) >> 32);         // of a turn, times 2^32
   float s, c;
   if (EXACT) {
-    sincospif((float)half * 4.656612873077393e-10f, &s, &c);         // 2^-31: half turns
+    // Less the nearest quarter turn, so that the argument's 24 bits are of an eighth of a turn at most: of half
+    // a turn, their rounding alone made the cosine's error 3.3e-8 rms.
+    const int q = (int)((unsigned)half + (1u << 29)) >> 30;
+    float s0, c0;
+    sincos_quarter((float)(int)((unsigned)half - ((unsigned)q << 30)) * 4.656612873077393e-10f, &s0, &c0);   // 2^-31
+    s = (q & 1) ? c0 : s0;
+    c = (q & 1) ? s0 : c0;
+    s = __uint_as_float(__float_as_uint(s) ^ (unsigned)(q & 2) << 30);
+    c = __uint_as_float(__float_as_uint(c) ^ (unsigned)((q + 1) & 2) << 30);
   } else {
     const float x = (float)half * 1.4629180792671596e-9f;            // 2^-31 pi: in [-pi, pi]
     s = __sinf(x);

@@ -291,3 +291,38 @@ def test_other_stream_and_graph():
     torch.cuda.synchronize()
     m = y.abs()[..., :64] + y.abs()[..., 64:]
     assert bool(((out - y).abs() <= 2.0 ** -18 * torch.cat([m, m], -1)).all())
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_fp32_rounds_like_fp32(layout, offset):
+    """fp32 results are as near to the exact ones as those of the same fp32 arithmetic with exactly
+    rounded cosines and sines.
+
+    In units of 2^-24 of |y| (u, w of variance 1): each rounded cosine and sine has a variance of 0.059
+    (measured over all angles; ulp^2 / 12), the two products' and the sum's roundings 0.27 together, so
+    plain arithmetic's is 0.39. The kernel's angle, an eighth of a turn at most in 24 bits, adds 0.27
+    of a rounding's variance, and a function good to one unit, uniform over 3/4 of it to either
+    side, has 2.25 of it: 0.059 * 2 * 2.25 * 1.27 + 0.27 = 0.61, a ratio of 1.25 in the norm. (A whole turn
+    in 24 bits has 5 times a rounding's variance: 1.49.)
+    """
+    g = torch.Generator().manual_seed(12)
+    T, H, D = 3000, 3, 128
+    x = torch.empty(T, H * D + offset)[:, offset:].unflatten(1, (H, D)).copy_(torch.randn(T, H, D, generator=g))
+    pos = torch.randint(-2 ** 20, 2 ** 20, (T,), generator=g, dtype=torch.int32)
+    a = pos.numpy().astype(np.float64)[:, None, None] * oracle.rope_angles(D)
+    c, s = np.cos(a), np.sin(a)
+    u, w = ((x[..., :64], x[..., 64:]) if layout == "half" else (x[..., 0::2], x[..., 1::2]))
+    u, w = u.numpy(), w.numpy()
+    dev = torch.empty(T, H * D + offset, device="cuda")[:, offset:].unflatten(1, (H, D)).copy_(x)
+    out = torch.empty_like(dev, memory_format=torch.contiguous_format)
+    for inverse in (False, True):
+        sn = -s if inverse else s
+        exact = np.stack([u * c - w * sn, w * c + u * sn])
+        c32, s32 = c.astype(np.float32), sn.astype(np.float32)
+        plain = np.stack([(np.float64(u) * c32 - np.float64(w * s32)), (np.float64(w) * c32 + np.float64(u * s32))])
+        bmw.la_rope(bmw.RopePlan.make(D, layout=layout), dev, pos.cuda(), out, inverse=inverse)
+        y = out.cpu().numpy()
+        y = np.stack([y[..., :64], y[..., 64:]] if layout == "half" else [y[..., 0::2], y[..., 1::2]])
+        err = [np.linalg.norm(v.astype(np.float32) - exact) / np.linalg.norm(exact) for v in (y, plain)]
+        assert err[0] <= 1.25 * err[1], err
