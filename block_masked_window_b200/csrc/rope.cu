@@ -8,8 +8,10 @@
 // interleaved one; channels from Rd on are copied. The inverse turns by -a.
 //
 // Angles: f_i is handed to the kernels as a 64-bit fraction of a turn, so that t f_i modulo a turn is
-// one wrapping integer product (error below 2^-33 turns at t = 2^31; in 64-bit floating point the
-// product, its reduction and the conversions took a third of the kernel's instructions). Sine and cosine
+// one wrapping integer product (in 64-bit floating point the product, its reduction and the
+// conversions took a third of the kernel's instructions). The product and its reduction add less than
+// 2^-31 turns; the plan's frequencies, doubles, are off by up to 2^-56 a position, 2^-24 turns (4e-7 of
+// an angle in radians) at 2^31 positions and 2^-38 at 2^17. Sine and cosine
 // are taken of it in 32 bits: for fp32 results of what is left of it after whole quarter turns, with an
 // error near a rounding's, and for 16-bit ones, whose rounding is 2^-12 of the value at best, of its
 // upper 32 bits with the fast functions (2^-21 absolute).
