@@ -181,9 +181,11 @@ __device__ __forceinline__ int kv_row(const Problem& p, int b, int h, int j) {
 // Issues the two (contiguous) or four (paged: one 64-row box per page piece) TMA loads of key
 // tile [jt, jt + 128) of segment sg into `dst`, all on barrier `fb`. Paged halves that lie
 // wholly past the segment's keys read the segment's last page instead (their rows are never
-// used), so no block-table entry beyond the sequence is touched. Every key tile is read once
-// per call and carries an L2 evict-first policy (paged, 64 ragged sequences: 40.5 us without it,
-// 37.4 us with it; the merge then finds the partials still in L2).
+// used), so no block-table entry beyond the sequence is touched. This kernel reads a tile once (the key
+// weights' kernel reads K again after it, and sequences whose tables share pages read those tiles once
+// each) and asks L2 to evict it first, so that the merge still finds the partials there. Paged, 64
+// ragged sequences: 39.9 us without it, 37.4 us with it, 62.8 and 59.1 us with key weights. Pages shared by
+// 64 sequences: 2048 keys 41.7 and 41.4 us, 8192 keys 92.4 and 92.8, 32768 keys 301.4 and 305.2.
 template <bool PAGED>
 __device__ __forceinline__ void load_kv_tile(const Problem& p, const Segment& sg,
                                              const CUtensorMap* map, uint32_t dst, uint32_t fb,
