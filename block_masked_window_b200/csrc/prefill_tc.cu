@@ -189,9 +189,19 @@ __global__ void __launch_bounds__(256) prefill_v16_kernel(PrefillProblem p) {
   const uint4* src = reinterpret_cast<const uint4*>(p.v + ((size_t)(b * p.Hkv + hk) * p.S + r0) * kHeadDim);
   uint4* dst = reinterpret_cast<uint4*>(p.v16 + ((size_t)(b * p.Hkv + hk) * p.Tp + r0) * kHeadDim);
   float vmax = 0.f;
-  for (int c = threadIdx.x; c < rows * (kHeadDim / 8); c += blockDim.x) {
-    const uint4 x = load_row16(src + c);   // 8 bf16
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  // (All loads in flight together: 300 tokens, both kernels: 12.7 us one at a time, 11.6 so.)
+  constexpr int kPer = kBN * (kHeadDim / 8) / 256;
+  const int n = rows * (kHeadDim / 8);
+  uint4 x[kPer];                               // of 8 bf16
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int c = threadIdx.x + 256 * i;
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (c < n) x[i] = load_row16(src + c);
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
     uint32_t o[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -200,7 +210,8 @@ __global__ void __launch_bounds__(256) prefill_v16_kernel(PrefillProblem p) {
       __half2 h2 = __floats2half2_rn(lo, hi);
       o[e] = *reinterpret_cast<uint32_t*>(&h2);
     }
-    dst[c] = make_uint4(o[0], o[1], o[2], o[3]);
+    const int c = threadIdx.x + 256 * i;
+    if (c < n) dst[c] = make_uint4(o[0], o[1], o[2], o[3]);
   }
   __shared__ float wmax[8];
   vmax = warp_max_f32(vmax);
