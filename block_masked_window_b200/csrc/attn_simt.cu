@@ -286,8 +286,6 @@ __global__ void __launch_bounds__(kThreads) pbd_attn_simt_kernel(Problem p) {
         packed.x = *reinterpret_cast<uint32_t*>(&o01);
         packed.y = *reinterpret_cast<uint32_t*>(&o23);
         *reinterpret_cast<uint2*>(p.out + out_row_offset(p, sg.b, sg.h, r) + d0) = packed;
-        if (p.lse2 && lane == 0)
-          p.lse2[((size_t)sg.b * p.Hkv + sg.h) * p.rows_pad + r] = s.m[r] + log2f(s.l[r]);
       } else {
         float* slot = slot_ptr(p, sg.slot);
         if (lane == 0) {
@@ -297,6 +295,10 @@ __global__ void __launch_bounds__(kThreads) pbd_attn_simt_kernel(Problem p) {
         *reinterpret_cast<float4*>(slot + 2 * p.rows_pad + (size_t)r * kHeadDim + d0) =
             make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
       }
+    }
+    if (p.lse2 && sg.whole) {   // (apart from the unrolled rows above, whose code it lengthened: 14 rows a window, 64 x 1000 keys 280 us, 276 so)
+      for (int r = tid; r < p.R; r += kThreads)
+        p.lse2[((size_t)sg.b * p.Hkv + sg.h) * p.rows_pad + r] = s.m[r] + log2f(s.l[r]);
     }
     __syncthreads();
   }
