@@ -11,7 +11,7 @@
 // probabilities in registers: no maximum, no exchange between threads, one store per key.
 //
 // Bound: the second reading of K from HBM (256 bytes per key against 4 to read and 4 to write of the
-// weights): 8 sequences of 32768 keys add 27 us to the attention's 50 us, of which the copy is 20.5
+// weights): 8 sequences of 32768 keys add 29.5 us to the attention's 49 us, of which the copy is 20.5
 // us at the measured rate. The exponentials (NQ per key, 16 per clock and SM) take a quarter of a
 // tile's copy time at NQ = 48. Leaving a share of K in L2 for this reading (evict-last in the attention
 // kernel, 40 to 134 MB of K) measured slower at every share (79.0 us without, 80.4 to 85.9 us with):
