@@ -83,3 +83,45 @@ def test_out_is_checked():
     v[0, 1, 44] += 1
     with pytest.raises(AssertionError):
         assert_parity(out, oracle.window_attention(q, k, v, lens, D ** -0.5))
+
+
+@pytest.mark.parametrize("page", [0, 64])
+def test_two_loops_at_once(page):
+    """Two loops with buffers and workspaces of their own, their steps queued on two streams without a
+    wait between them: the bits of the same loops one after the other."""
+    def loops():
+        out = []
+        for seed, prompt in ((5, [90, 10]), (6, [40, 120, 0])):
+            L = Loop(prompt, page, seed)
+            for c in (L.k, L.v):
+                c.copy_(torch.randn(c.shape, generator=torch.Generator().manual_seed(seed)))
+            L.lens.copy_(torch.tensor(prompt, dtype=torch.int32))
+            L.pos.copy_(L.lens)
+            L.key_pos.copy_(torch.arange(L.S, dtype=torch.int32).expand(L.B, HKV, L.S))
+            L.draw()
+            out.append(L)
+        torch.cuda.synchronize()
+        return out
+
+    def state(L):
+        torch.cuda.synchronize()
+        return [t.clone() for t in (L.k, L.v, L.weights, L.key_pos, L.lens, L.pos, L.q_rot, L.out, L.tokens, L.acc)]
+
+    want = []
+    for L in loops():
+        for _ in range(40):
+            L.step()
+            L.evict(128)
+        want.append(state(L))
+    for _ in range(3):
+        both = loops()
+        streams = [torch.cuda.Stream() for _ in both]
+        for _ in range(40):
+            for L, s in zip(both, streams):
+                with torch.cuda.stream(s):
+                    L.step()
+                    L.evict(128)
+        for L, w in zip(both, want):
+            for a, b in zip(state(L), w):
+                assert torch.equal(a, b)
+            assert bmw.la_pbd_check(L.ws) == 0 and bmw.la_pbd_check(L.ews) == 0
